@@ -1,4 +1,5 @@
-"""bit_moe_amd: the 2-bit (and MXFP4) routed-expert MoE FFN layer on MI355X (gfx950).
+"""bit_moe_amd: the 2-bit (and MXFP4) routed-expert MoE FFN layer on MI355X (gfx950),
+and the operators of the same layer with 16-bit experts and their gradients.
 
 Python binding over libbitmoe.so (see include/bitmoe.h).  PyTorch provides
 device memory and streams only; every step of the layer runs in the
@@ -9,6 +10,8 @@ from ._lib import (BF16, BitMoEError, DECODE, ExpertCache, F32, FORMAT_2BIT, FOR
                    forward_decode, forward_decode_noalloc, lib, lib_checked, quantize_iq2x, quantize_mxfp4, quantize_q2k, pack_bf16, pack_iq2x,
                    pack_mxfp4, pack_q2k, route, route_workspace_bytes, set_timing_events, strerror, topk, version,
                    workspace_bytes)
+from .experts import (ACTS, MATMUL, MATMUL_DW, MATMUL_DX, combine, combine_backward, expert_matmul, expert_matmul_dw,
+                      expert_matmul_dx, expert_matmul_workspace_bytes, linear, linear_backward, swiglu, swiglu_backward)
 
 
 def layer_from_canonical(H, I, E, k, router_bits, gate, up, down, grid, shared=None, device="cuda",
@@ -44,8 +47,10 @@ def layer_from_canonical(H, I, E, k, router_bits, gate, up, down, grid, shared=N
     return Layer(H, I, E, k, router, gq, uq, dq, g, sh, fmt=fmt)
 
 
-__all__ = ["BF16", "BitMoEError", "DECODE", "ExpertCache", "F32", "FORMAT_2BIT", "FORMAT_MXFP4", "Layer", "PREFILL",
+__all__ = ["ACTS", "BF16", "BitMoEError", "DECODE", "ExpertCache", "F32", "FORMAT_2BIT", "FORMAT_MXFP4", "Layer", "PREFILL",
            "SYMBOLS", "TIME_DOWN", "TIME_GATEUP", "bucket", "dequant_iq2x", "dequant_mxfp4", "dequant_q2k", "ffn_decode",
            "ffn_prefill", "forward_decode", "forward_decode_noalloc", "layer_from_canonical", "lib_checked", "quantize_iq2x",
            "quantize_mxfp4", "quantize_q2k", "lib", "pack_bf16", "pack_iq2x", "pack_mxfp4", "pack_q2k", "route", "route_workspace_bytes",
-           "set_timing_events", "strerror", "topk", "version", "workspace_bytes"]
+           "set_timing_events", "strerror", "topk", "version", "workspace_bytes",
+           "MATMUL", "MATMUL_DW", "MATMUL_DX", "combine", "combine_backward", "expert_matmul", "expert_matmul_dw",
+           "expert_matmul_dx", "expert_matmul_workspace_bytes", "linear", "linear_backward", "swiglu", "swiglu_backward"]

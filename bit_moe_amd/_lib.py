@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbitmoe.so")
 LIB_CHECKED_PATH = os.path.join(HERE, "libbitmoe_checked.so")    # built with BITMOE_CHECK_IDS = 1
 
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2          # F16: the 16-bit expert layer (experts.py) only
 DECODE, PREFILL = 0, 1
 LAYOUT_CANONICAL, LAYOUT_TILED = 0, 1
 FORMAT_2BIT, FORMAT_MXFP4 = 0, 1
@@ -34,6 +34,9 @@ SYMBOLS = [
     "moe_set_timing_events", "moe_strerror", "moe_version",
     "moe_cache_pool_bytes", "moe_cache_create", "moe_cache_layer", "moe_cache_map", "moe_cache_stats",
     "moe_cache_destroy",
+    "moe_expert_matmul_workspace_bytes", "moe_expert_matmul", "moe_expert_matmul_dx", "moe_expert_matmul_dw",
+    "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward_workspace_bytes", "moe_linear_backward",
+    "moe_swiglu", "moe_swiglu_backward", "moe_combine", "moe_combine_backward",
 ]
 
 
@@ -43,6 +46,16 @@ class LayerStruct(C.Structure):
                 ("down_q", C.c_void_p), ("grid", C.c_void_p), ("shared_gate", C.c_void_p),
                 ("shared_up", C.c_void_p), ("shared_down", C.c_void_p), ("layout", C.c_int32),
                 ("format", C.c_int32)]
+
+
+class RowsStruct(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("map", C.c_void_p), ("ld", C.c_int64), ("rows", C.c_int32),
+                ("cols", C.c_int32), ("div", C.c_int32), ("dtype", C.c_int32)]
+
+
+class ExpertsStruct(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("ld", C.c_int64), ("stride", C.c_int64), ("E", C.c_int32),
+                ("N", C.c_int32), ("K", C.c_int32), ("dtype", C.c_int32)]
 
 
 _lib = None
@@ -79,7 +92,7 @@ def _load(path: str) -> C.CDLL:
         raise ImportError(f"{path} is not built; run `python -m bit_moe_amd.build`")
     L = C.CDLL(path)
     P, I, I64, SZ = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
-    LP = C.POINTER(LayerStruct)
+    LP, RP, EP = C.POINTER(LayerStruct), C.POINTER(RowsStruct), C.POINTER(ExpertsStruct)
     sig = {
         "moe_route_workspace_bytes": ([LP, I, I], SZ),
         "moe_route": ([LP, P, I, I, P, P, P, P, SZ, P], I),
@@ -110,6 +123,18 @@ def _load(path: str) -> C.CDLL:
         "moe_cache_stats": ([P, C.POINTER(C.c_int64), C.POINTER(C.c_int64), P], I),
         "moe_cache_destroy": ([P], I),
         "moe_version": ([], C.c_char_p),
+        "moe_expert_matmul_workspace_bytes": ([I, I, I, I, I], SZ),
+        "moe_expert_matmul": ([RP, EP, P, I, RP, P, SZ, P], I),
+        "moe_expert_matmul_dx": ([RP, EP, P, I, RP, P, SZ, P], I),
+        "moe_expert_matmul_dw": ([RP, RP, P, I, EP, I, P, SZ, P], I),
+        "moe_linear_workspace_bytes": ([I, I, I], SZ),
+        "moe_linear": ([RP, EP, P, I, RP, RP, RP, P, SZ, P], I),
+        "moe_linear_backward_workspace_bytes": ([I, I, I], SZ),
+        "moe_linear_backward": ([RP, RP, EP, I, RP, RP, EP, P, I, P, SZ, P], I),
+        "moe_swiglu": ([RP, RP, RP, P], I),
+        "moe_swiglu_backward": ([RP, RP, RP, RP, RP, P], I),
+        "moe_combine": ([RP, P, I, I, RP, RP, P], I),
+        "moe_combine_backward": ([RP, RP, P, I, I, RP, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)

@@ -1,0 +1,70 @@
+// Host-side interface of the 16-bit expert layer: the arguments that the C
+// ABI's checks (experts.cpp) hand to the launchers in experts_*.hip.
+#pragma once
+
+#include "host.h"
+
+namespace bm_host {
+
+// Rows of a matrix.  Row r of the call is matrix row r, or map[r] / div;
+// a row outside [0, rows) reads as zeros and is not written.
+struct GemmRows {
+    const void *p;
+    const int32_t *map;
+    int64_t ld;
+    int32_t rows, div;
+};
+
+// C[m][n] = sum_k A[m][k] B[n][k] over the groups of rows that `offsets`
+// marks, in three layouts.
+enum GemmLayout {
+    kForward = 0,       // A = x rows (K columns),  B = W_e[n][k]:       C rows = y rows
+    kGradRows = 1,      // A = dy rows (contracted), B = W_e[k][n]:      C rows = dx rows
+    kGradWeights = 2,   // A = dy rows, B = x rows, contracted over the group's rows: C = dW_e[m][n]
+};
+struct GemmArgs {
+    GemmRows a, b;             // kForward, kGradRows: b is the weights, without a map
+    int64_t b_stride;          // elements between experts
+    GemmRows c;                // (p is written)
+    int64_t c_stride;          // kGradWeights: elements between experts
+    const int32_t *offsets;    // device [E+1]; NULL: one group of R rows
+    int32_t E, R;
+    int32_t M, N, K;           // M: kGradWeights only (elsewhere the group's rows);
+                               // K: not kGradWeights (there the group's rows)
+    int32_t c_dtype;
+    int32_t accumulate;        // kGradWeights: add to what is there
+    // epilogue: C = act(sum + bias) + res, the value before act kept in pre
+    int32_t act;
+    const void *bias, *res;
+    void *pre;
+    int64_t ld_res, ld_pre;
+    int32_t bias_dtype, res_dtype, pre_dtype;
+};
+
+// workspace of a product: a rule on the host-known sizes (E, R, M, N, K)
+size_t gemm_ws_bytes(int layout, const GemmArgs &g);
+int launch_gemm(int layout, int dtype, const GemmArgs &g, void *ws, hipStream_t s);
+
+// dz = dy act'(pre) (dz may be NULL) and, with db, its column sums by slices
+// of rows (partial [slices][N])
+struct ActBackward {
+    const void *dy, *pre;
+    void *dz;
+    int64_t ld_dy, ld_pre, ld_dz;
+    int32_t T, N, act;
+    void *db;
+    int32_t db_dtype;
+    float *partial;
+};
+int act_backward_slices(int T, int N);
+int launch_act_backward(const ActBackward &p, int dtype, hipStream_t s);
+
+int launch_swiglu(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows &h, int dtype, hipStream_t s);
+int launch_swiglu_backward(const bitmoe_rows &dh, const bitmoe_rows &gate, const bitmoe_rows &up,
+                           const bitmoe_rows &dgate, const bitmoe_rows &dup, int dtype, hipStream_t s);
+int launch_combine(const bitmoe_rows &o, const float *w, int T, int k, const bitmoe_rows *residual,
+                   const bitmoe_rows &y, hipStream_t s);
+int launch_combine_backward(const bitmoe_rows &dy, const bitmoe_rows *o, const float *w, int T, int k,
+                            const bitmoe_rows *d_o, float *dw, int dtype, hipStream_t s);
+
+}  // namespace bm_host

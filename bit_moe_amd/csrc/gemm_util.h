@@ -1,0 +1,334 @@
+// Device helpers of the 16-bit matrix products: element types, tiles in LDS,
+// matrix-core operands, the search for a workgroup's tile, the epilogue.
+#pragma once
+
+#include "common.h"
+#include "experts.h"
+
+namespace bm {
+
+using bm_host::GemmArgs;
+using bm_host::GemmRows;
+using bm_host::kForward;
+using bm_host::kGradRows;
+using bm_host::kGradWeights;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kBK = 64;             // contraction per stage
+
+// ---- elements -------------------------------------------------------------
+// DT: BITMOE_BF16 or BITMOE_F16
+template <int DT>
+BM_DEV f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
+    if constexpr (DT == BITMOE_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
+                                                       c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                      0, 0, 0);
+}
+BM_DEV float elem_f32(uint32_t bits, int dtype) { return dtype == BITMOE_BF16 ? bf16_to_f32(bits) : fp16_to_f32(bits); }
+BM_DEV uint32_t elem_bits(float v, int dtype) { return dtype == BITMOE_BF16 ? f32_to_bf16_rne(v) : f16_bits(v); }
+
+// 16, 8 and 4 bytes at any element's address: gfx950 reads and writes global
+// memory at any alignment, so rows need not be aligned to a vector
+struct __attribute__((packed, aligned(2))) U128 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(2))) U64 { uint32_t w[2]; };
+struct __attribute__((packed, aligned(4))) F128 { float w[4]; };
+
+BM_DEV uint4 load16(const uint16_t *p) {
+    const U128 u = *reinterpret_cast<const U128 *>(p);
+    return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+}
+// elements [0, n) of 8, the rest zero
+BM_DEV uint4 load16_part(const uint16_t *p, int n) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// four consecutive values of a row, the first n of them (n >= 1)
+BM_DEV void load4(const void *p, int64_t i, int n, int dtype, float *v) {
+    if (dtype == BITMOE_F32) {
+        const float *q = static_cast<const float *>(p) + i;
+        if (n >= 4) {
+            const F128 u = *reinterpret_cast<const F128 *>(q);
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[j] = u.w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[j] = j < n ? q[j] : 0.f;
+        }
+        return;
+    }
+    const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+    if (n >= 4) {
+        const U64 u = *reinterpret_cast<const U64 *>(q);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = elem_f32(u.w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, dtype);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = j < n ? elem_f32(q[j], dtype) : 0.f;
+    }
+}
+BM_DEV void store4(void *p, int64_t i, int n, int dtype, const float *v) {
+    if (dtype == BITMOE_F32) {
+        float *q = static_cast<float *>(p) + i;
+        if (n >= 4) {
+            *reinterpret_cast<F128 *>(q) = F128{{v[0], v[1], v[2], v[3]}};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (j < n) q[j] = v[j];
+        }
+        return;
+    }
+    uint16_t *q = static_cast<uint16_t *>(p) + i;
+    if (n >= 4) {
+        *reinterpret_cast<U64 *>(q) = U64{{elem_bits(v[0], dtype) | elem_bits(v[1], dtype) << 16,
+                                           elem_bits(v[2], dtype) | elem_bits(v[3], dtype) << 16}};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (j < n) q[j] = (uint16_t)elem_bits(v[j], dtype);
+    }
+}
+
+// eight consecutive values of a row, the first n of them (n >= 1; the rest 0)
+BM_DEV void load8(const void *p, int64_t i, int n, int dtype, float *v) {
+    if (dtype == BITMOE_F32) {
+        load4(p, i, n, dtype, v);
+        if (n > 4) load4(p, i + 4, n - 4, dtype, v + 4);
+        else v[4] = v[5] = v[6] = v[7] = 0.f;
+        return;
+    }
+    const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+    const uint4 u = n >= 8 ? load16(q) : load16_part(q, n);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = elem_f32(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, dtype);
+}
+BM_DEV void store8(void *p, int64_t i, int n, int dtype, const float *v) {
+    if (dtype != BITMOE_F32 && n >= 8) {
+        U128 u;
+#pragma unroll
+        for (int j = 0; j < 4; j++) u.w[j] = elem_bits(v[2 * j], dtype) | elem_bits(v[2 * j + 1], dtype) << 16;
+        *reinterpret_cast<U128 *>(static_cast<uint16_t *>(p) + i) = u;
+        return;
+    }
+    store4(p, i, n, dtype, v);
+    if (n > 4) store4(p, i + 4, n - 4, dtype, v + 4);
+}
+
+// ---- rows and groups ------------------------------------------------------
+// matrix row of the call's row r, or -1
+BM_DEV int row_of(const GemmRows &q, int r) {
+    int m = r;
+    if (q.map) {
+        m = q.map[r];
+        if (m < 0) return -1;
+        if (q.div > 1) m = (int)((uint32_t)m / (uint32_t)q.div);
+    }
+    return m < q.rows ? m : -1;
+}
+// first row of group e (and of e + 1: its end), kept inside the call's rows
+BM_DEV int group_start(const GemmArgs &g, int e) {
+    if (!g.offsets) return e ? g.R : 0;
+    return min(max(g.offsets[e], 0), g.R);
+}
+
+struct Tile {
+    int e, r0, r1;      // expert, its rows
+    int m, n;           // tile indexes
+};
+
+// A workgroup's tile among the (expert, row tile, column tile) of the groups.
+// Every wave finds it by itself: each lane counts the row tiles of a run of
+// experts, a scan over the lanes gives their places.  Workgroups go round
+// the 8 XCDs in turn, so consecutive tiles are given to workgroups of one
+// XCD, whose L2 then serves the operands they share; within an expert, 8 row
+// tiles by all column tiles at a time.
+template <int BM>
+BM_DEV bool find_tile(const GemmArgs &g, int nt, int bid, Tile *t) {
+    const int lane = lane_id(), per = (g.E + 63) / 64;
+    int mine = 0;
+    for (int i = 0; i < per; i++) {
+        const int e = lane * per + i;
+        if (e < g.E) mine += (max(group_start(g, e + 1) - group_start(g, e), 0) + BM - 1) / BM;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(incl, o, kWave);
+        if (lane >= o) incl += v;
+    }
+    const int total = __shfl(incl, 63, kWave);
+    const int64_t items = (int64_t)total * nt;
+    const int64_t per_xcd = (items + 7) / 8;
+    const int64_t item = (int64_t)(bid & 7) * per_xcd + (bid >> 3);
+    if ((bid >> 3) >= per_xcd || item >= items) return false;
+    const int mt = (int)(item / nt);         // as a place among the row tiles
+    const uint64_t has = __ballot(mt < incl);
+    const int src = __builtin_ctzll(has);    // the first lane whose run reaches past it
+    int base = __shfl(incl - mine, src, kWave), e = src * per;
+    int cnt, r0, r1;
+    for (;; e++) {
+        r0 = group_start(g, e);
+        r1 = group_start(g, e + 1);
+        cnt = (max(r1 - r0, 0) + BM - 1) / BM;
+        if (mt < base + cnt || e >= g.E - 1) break;
+        base += cnt;
+    }
+    const int idx = (int)(item - (int64_t)base * nt);
+    const int blk = idx / (8 * nt), mb = min(8, cnt - 8 * blk), rem = idx - blk * 8 * nt;
+    t->e = __builtin_amdgcn_readfirstlane(e);
+    t->r0 = __builtin_amdgcn_readfirstlane(r0);
+    t->r1 = __builtin_amdgcn_readfirstlane(r1);
+    t->m = __builtin_amdgcn_readfirstlane(8 * blk + rem % mb);
+    t->n = __builtin_amdgcn_readfirstlane(rem / mb);
+    return true;
+}
+// the same for the weights' gradient, whose tiles are fixed: (expert, 8 row
+// tiles by all column tiles at a time)
+BM_DEV bool find_tile_dw(const GemmArgs &g, int mt, int nt, int bid, Tile *t) {
+    const int64_t items = (int64_t)g.E * mt * nt, per_xcd = (items + 7) / 8;
+    const int64_t item = (int64_t)(bid & 7) * per_xcd + (bid >> 3);
+    if ((bid >> 3) >= per_xcd || item >= items) return false;
+    t->e = (int)(item / ((int64_t)mt * nt));
+    const int idx = (int)(item - (int64_t)t->e * mt * nt);
+    const int blk = idx / (8 * nt), mb = min(8, mt - 8 * blk), rem = idx - blk * 8 * nt;
+    t->m = 8 * blk + rem % mb;
+    t->n = rem / mb;
+    t->r0 = group_start(g, t->e);
+    t->r1 = max(group_start(g, t->e + 1), t->r0);
+    return true;
+}
+
+// ---- tiles in LDS ---------------------------------------------------------
+// An operand's stage is X rows of kBK elements (contiguous along the
+// contraction: KC) or kBK rows of X elements (KS), in 16-byte pieces.
+//  KC: piece c of row r at slot c ^ (r & 7) of the row's 8: the 16-byte reads
+//      of 8 consecutive rows, one piece each, fall on different banks.
+//  KS: pieces move in pairs of 32 bytes, pair c of row k at c ^ swz(k): a
+//      transposed read takes 32 bytes of each of 4 consecutive rows (8, 16, 24
+//      rows further for the wave's other lanes), and these fall on different
+//      banks too.
+template <int X>
+BM_DEV int ks_swz(int k) {
+    return X >= 128 ? (k & 3) | ((k >> 1) & 4) : (k & 3);
+}
+// piece p of the stage (in LDS order): its row and its piece in the row
+template <bool KC, int X>
+BM_DEV void piece_at(int p, int *row, int *col) {
+    if (KC) {
+        *row = p >> 3;
+        *col = (p & 7) ^ (*row & 7);
+    } else {
+        *row = p / (X / 8);
+        const int s = p % (X / 8);
+        *col = ((s >> 1) ^ ks_swz<X>(*row)) << 1 | (s & 1);
+    }
+}
+// the wave's matrix-core operand: 16 rows (KC) or columns (KS) from x0, 32 of
+// the contraction from kk; lane l holds row l % 16, contraction 8 (l / 16) + j
+template <bool KC, int X>
+BM_DEV s16x8 frag(const uint16_t *tile, int x0, int kk, int lane) {
+    const int i = lane & 15, q = lane >> 4;
+    if (KC) {
+        const int row = x0 + i;
+        return *reinterpret_cast<const s16x8 *>(tile + row * kBK + ((((kk >> 3) + q) ^ (row & 7)) << 3));
+    } else {
+        // a transposing read: 16 lanes give 4 rows of 16 elements, four lanes
+        // a row, and receive the 16 columns, 4 elements each
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const int k = kk + 8 * q + (i >> 2);
+        const uint16_t *p = tile + k * X + (((x0 >> 4) ^ ks_swz<X>(k)) << 4) + ((i & 3) << 2);
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(tile + (k + 4) * X + (((x0 >> 4) ^ ks_swz<X>(k + 4)) << 4) + ((i & 3) << 2)));
+        return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+}
+
+// ---- epilogue -------------------------------------------------------------
+BM_DEV float act_fwd(float z, int act) {
+    switch (act) {
+        case BITMOE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
+        case BITMOE_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+        case BITMOE_ACT_GELU_TANH: {
+            // 0.5 (1 + tanh u) = 1 / (1 + e^-2u)
+            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
+            return z / (1.f + __expf(-2.f * u));
+        }
+        case BITMOE_ACT_SILU: return z / (1.f + __expf(-z));
+        default: return z;
+    }
+}
+
+// d act / dz
+BM_DEV float act_slope(float z, int act) {
+    switch (act) {
+        case BITMOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+        case BITMOE_ACT_GELU:
+            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+        case BITMOE_ACT_GELU_TANH: {
+            // with p = 1 / (1 + e^-2u): p + 2 z p (1 - p) du/dz
+            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z), p = 1.f / (1.f + __expf(-2.f * u));
+            return p + 2.f * z * p * (1.f - p) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+        }
+        case BITMOE_ACT_SILU: {
+            const float p = 1.f / (1.f + __expf(-z));
+            return p + z * p * (1.f - p);
+        }
+        default: return 1.f;
+    }
+}
+
+// four outputs (m fixed, n.. n+3) of a tile
+template <int LAY>
+BM_DEV void finish4(const GemmArgs &g, int e, int m, int n, float *v) {
+    const int left = g.N - n;
+    if (left <= 0) return;
+    if constexpr (LAY == kGradWeights) {
+        const int64_t at = (int64_t)e * g.c_stride + (int64_t)m * g.c.ld + n;
+        if (g.accumulate) {
+            float o[4];
+            load4(g.c.p, at, left, g.c_dtype, o);
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[j] += o[j];
+        }
+        store4(const_cast<void *>(g.c.p), at, left, g.c_dtype, v);
+    } else {
+        const int row = row_of(g.c, m);
+        if (row < 0) return;
+        if constexpr (LAY == kForward) {
+            if (g.bias) {
+                float o[4];
+                load4(g.bias, n, left, g.bias_dtype, o);
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] += o[j];
+            }
+            if (g.pre) store4(g.pre, (int64_t)row * g.ld_pre + n, left, g.pre_dtype, v);
+            if (g.act != BITMOE_ACT_NONE) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] = act_fwd(v[j], g.act);
+            }
+            if (g.res) {
+                float o[4];
+                load4(g.res, (int64_t)row * g.ld_res + n, left, g.res_dtype, o);
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] += o[j];
+            }
+        }
+        store4(const_cast<void *>(g.c.p), (int64_t)row * g.c.ld + n, left, g.c_dtype, v);
+    }
+}
+
+}  // namespace bm

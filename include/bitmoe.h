@@ -136,6 +136,7 @@ extern "C" {
 
 #define BITMOE_F32  0   /* float32 activations / outputs */
 #define BITMOE_BF16 1   /* bfloat16 activations / outputs */
+#define BITMOE_F16  2   /* float16 (the 16-bit expert layer's calls only) */
 
 #define BITMOE_DECODE  0
 #define BITMOE_PREFILL 1
@@ -429,6 +430,139 @@ int moe_pack_iq2x(const void *src, void *dst, int E, int N, int K, void *stream)
 int moe_pack_q2k(const void *src, void *dst, int E, int N, int K, void *stream);
 int moe_pack_bf16(const void *src, void *dst, int N, int K, void *stream);
 int moe_pack_mxfp4(const void *src, void *dst, int E, int N, int K, void *stream);
+
+/*
+ * The layer with 16-bit experts, and its gradients: what trains or calibrates
+ * the routed experts before moe_quantize_* takes them, and runs them
+ * unquantised (the released weights are wider than 2 bits: "ds4 : analyse
+ * pratique ...", section "Support de modeles et choix de quantification").
+ * Products over experts take the groups that moe_bucket gives, so an expert
+ * layer is moe_route, moe_bucket, then
+ *   gate|up  z = moe_expert_matmul(x by perm / k, W_gu)    (bucket order)
+ *            h = moe_swiglu(z halves)
+ *   down     o = moe_expert_matmul(h, W_d, o by perm)      (pair order t*k+j)
+ *            y = moe_combine(o, w, residual)
+ * and backward moe_combine_backward, moe_expert_matmul_dx / _dw (dy by perm),
+ * moe_swiglu_backward, _dx / _dw again, and moe_combine without weights over
+ * the pairs' dx.
+ *
+ * Conventions beyond those above
+ *  - Element types: BITMOE_BF16 or BITMOE_F16, one type for all 16-bit
+ *    operands of a call; outputs named below may be BITMOE_F32 instead.
+ *    Products accumulate in fp32 on the matrix cores and are rounded once, to
+ *    the output's type.
+ *  - Any size from 1: rows R <= 2^24, N and K <= 2^18, and any row stride
+ *    ld >= cols (in elements).  Pointers are aligned to their element (maps:
+ *    4 bytes); rows whose addresses are all multiples of 16 bytes run fastest.
+ *  - A bitmoe_rows is a matrix of `rows` x `cols`.  With map (device int32
+ *    [R]) the call's row r is matrix row map[r] / div (rounded down);
+ *    without, row r.  A map entry that is negative, or whose row lies outside
+ *    [0, rows), means no row: an input reads as zeros, an output row is not
+ *    written.  Output rows of a call must be distinct.
+ *  - offsets: device int32 [E+1], ascending: rows offsets[e] .. offsets[e+1]
+ *    of the call belong to expert e.  Values are clamped to [0, R]; rows in no
+ *    group (behind the last one) are neither read nor written.
+ *  - Outputs must not overlap inputs, except where a call says so.
+ *  - Results do not depend on scheduling (no atomics; sums in a fixed order).
+ * Errors of all calls: EINVAL (null or misaligned pointer, size < 1 where
+ * one is needed, ld < cols, sizes or types of the operands that do not agree),
+ * EUNSUPPORTED (sizes above the limits), EWORKSPACE, EHIP.
+ */
+#define BITMOE_ACT_NONE      0
+#define BITMOE_ACT_RELU      1
+#define BITMOE_ACT_GELU      2   /* z/2 (1 + erf(z / sqrt 2)) */
+#define BITMOE_ACT_GELU_TANH 3   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define BITMOE_ACT_SILU      4   /* z / (1 + e^-z) */
+
+typedef struct bitmoe_rows {
+    void *data;            /* row i, column c at element i * ld + c */
+    const int32_t *map;    /* NULL, or device int32 [R] */
+    int64_t ld;
+    int32_t rows, cols;
+    int32_t div;           /* >= 1; used with a map */
+    int32_t dtype;
+} bitmoe_rows;
+
+typedef struct bitmoe_experts {
+    void *data;            /* W_e[n][k] at element e * stride + n * ld + k */
+    int64_t ld, stride;    /* ld >= K; stride >= N * ld when E > 1 */
+    int32_t E, N, K;
+    int32_t dtype;
+} bitmoe_experts;
+
+/*
+ * Matrix products grouped by expert, for the R rows of each call:
+ *  moe_expert_matmul     y[r] = W_e x[r]        (x: K columns, y: N)
+ *  moe_expert_matmul_dx  dx[r] = W_e^T dy[r]    (dy: N columns, dx: K)
+ *  moe_expert_matmul_dw  dW_e = sum over e's rows r of dy[r] x[r]^T (N x K; 0
+ *     for an expert without rows), added to what dw holds if accumulate != 0
+ * with e the expert whose group row r lies in.  y, dx and dw may be
+ * BITMOE_F32.  R = 0 does nothing (moe_expert_matmul_dw: every dW_e is 0).
+ * E <= 1024.  ws: moe_expert_matmul_workspace_bytes(op, E, R, N, K) bytes of
+ * device memory, 256-byte aligned (op BITMOE_MATMUL_*; N, K those of the
+ * experts; 0: none needed).
+ */
+#define BITMOE_MATMUL    0
+#define BITMOE_MATMUL_DX 1
+#define BITMOE_MATMUL_DW 2
+size_t moe_expert_matmul_workspace_bytes(int op, int E, int R, int N, int K);
+int moe_expert_matmul(const bitmoe_rows *x, const bitmoe_experts *w, const int32_t *offsets, int R,
+                      const bitmoe_rows *y, void *ws, size_t ws_bytes, void *stream);
+int moe_expert_matmul_dx(const bitmoe_rows *dy, const bitmoe_experts *w, const int32_t *offsets, int R,
+                         const bitmoe_rows *dx, void *ws, size_t ws_bytes, void *stream);
+int moe_expert_matmul_dw(const bitmoe_rows *dy, const bitmoe_rows *x, const int32_t *offsets, int R,
+                         const bitmoe_experts *dw, int accumulate, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/*
+ * Dense product with an epilogue (the shared expert's projections):
+ *     z = x W^T + bias;  y = act(z) + residual
+ * x [T][K], w with E = 1 [N][K], bias [N] of x's type or NULL, residual
+ * [T][N] of x's type or BITMOE_F32 or NULL, y [T][N] of x's type or
+ * BITMOE_F32 (y may be the residual itself: same address, ld and type).  pre
+ * [T][N] of x's type (or NULL) receives z for the backward pass.  No maps.
+ * Backward, given dy [T][N] of x's type and (act != BITMOE_ACT_NONE) pre:
+ *     dz = dy act'(pre);  dx = dz W;  dW = dz^T x;  db = column sums of dz
+ * each written if its pointer is not NULL (dx, dw of x's type or BITMOE_F32,
+ * db [N] of db_dtype); the residual's gradient is dy.  dz enters the products
+ * rounded to x's type, and db before that rounding.  ReLU has slope 0 at 0.
+ * ws: moe_linear_workspace_bytes(T, N, K), moe_linear_backward_workspace_bytes
+ * (T, N, K) bytes, 256-byte aligned.  T = 0 does nothing (dw and db are 0).
+ */
+size_t moe_linear_workspace_bytes(int T, int N, int K);
+int moe_linear(const bitmoe_rows *x, const bitmoe_experts *w, const void *bias, int act,
+               const bitmoe_rows *residual, const bitmoe_rows *pre, const bitmoe_rows *y, void *ws,
+               size_t ws_bytes, void *stream);
+size_t moe_linear_backward_workspace_bytes(int T, int N, int K);
+int moe_linear_backward(const bitmoe_rows *dy, const bitmoe_rows *x, const bitmoe_experts *w, int act,
+                        const bitmoe_rows *pre, const bitmoe_rows *dx, const bitmoe_experts *dw,
+                        void *db, int db_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The gated activation between an expert's products, h = silu(gate) * up, and
+ * its gradients dgate = dh up silu'(gate), dup = dh silu(gate).  All [R][I] of
+ * one 16-bit type, each with its own ld (gate and up may be the halves of one
+ * [R][2I] matrix).  No maps.  An output may be an input itself (same address
+ * and ld).  R = 0 does nothing.
+ */
+int moe_swiglu(const bitmoe_rows *gate, const bitmoe_rows *up, const bitmoe_rows *h, void *stream);
+int moe_swiglu_backward(const bitmoe_rows *dh, const bitmoe_rows *gate, const bitmoe_rows *up,
+                        const bitmoe_rows *dgate, const bitmoe_rows *dup, void *stream);
+
+/*
+ * Weighted combine of a token's k expert rows (pair order, as the layer's
+ * last step): y[t] = sum_j w[t][j] o[t*k+j] + residual[t], and its gradients
+ * d_o[t*k+j] = w[t][j] dy[t], dw[t][j] = <dy[t], o[t*k+j]> (the residual's is
+ * dy).  o, d_o [T*k][H] of a 16-bit type; residual, y, dy [T][H] of that type
+ * or BITMOE_F32; w, dw float32 [T][k], w NULL: all ones; residual may be NULL;
+ * of d_o and dw one may be NULL (o may be NULL without dw).  1 <= k <= 16.  No
+ * maps.  y may be the residual itself and d_o may be o itself (same address,
+ * ld and type).  T = 0 does nothing.
+ */
+int moe_combine(const bitmoe_rows *o, const float *w, int T, int k, const bitmoe_rows *residual,
+                const bitmoe_rows *y, void *stream);
+int moe_combine_backward(const bitmoe_rows *dy, const bitmoe_rows *o, const float *w, int T, int k,
+                         const bitmoe_rows *d_o, float *dw, void *stream);
 
 /*
  * Measurement hook.  When start and stop are both hipEvent_t handles (passed
