@@ -51,8 +51,20 @@ int check_ws(void *ws, size_t have, size_t need) {
     return BITMOE_OK;
 }
 
-GemmRows rows_arg(const bitmoe_rows *m) { return GemmRows{m->data, m->map, m->ld, m->rows, m->div}; }
-GemmRows weights_arg(const bitmoe_experts *w) { return GemmRows{w->data, nullptr, w->ld, w->N, 1}; }
+// Division by an invariant: with 2^(s-1) < d <= 2^s, m = floor(2^(31+s) / d) + 1
+// gives floor(x / d) = floor(x m / 2^(31+s)) for every x < 2^31 (the excess
+// m d - 2^(31+s) is at most d <= 2^s, so x times it stays below 2^(31+s)).
+GemmRows rows_arg(const bitmoe_rows *m) {
+    GemmRows r{m->data, m->map, m->ld, m->rows, 0, 0};
+    if (m->map && m->div > 1) {
+        uint32_t s = 0;
+        while (((uint64_t)1 << s) < (uint64_t)m->div) s++;
+        r.mul = (uint32_t)(((uint64_t)1 << (31 + s)) / (uint64_t)m->div + 1);
+        r.shift = s - 1;
+    }
+    return r;
+}
+GemmRows weights_arg(const bitmoe_experts *w) { return GemmRows{w->data, nullptr, w->ld, w->N, 0, 0}; }
 
 // y = W x or dx = W^T dy over groups
 GemmArgs rows_product(const bitmoe_rows *a, const bitmoe_experts *w, const int32_t *offsets, int R,
@@ -67,7 +79,7 @@ GemmArgs rows_product(const bitmoe_rows *a, const bitmoe_experts *w, const int32
     g.R = R;
     g.N = dx ? w->K : w->N;
     g.K = dx ? w->N : w->K;
-    g.c_dtype = c->dtype;
+    g.c_f32 = c->dtype == BITMOE_F32;
     return g;
 }
 
@@ -83,8 +95,8 @@ GemmArgs weights_product(const bitmoe_rows *dy, const bitmoe_rows *x, const int3
     g.R = R;
     g.M = dw->N;
     g.N = dw->K;
-    g.c_dtype = dw->dtype;
-    g.accumulate = accumulate;
+    g.c_f32 = dw->dtype == BITMOE_F32;
+    g.accumulate = accumulate != 0;
     return g;
 }
 
@@ -192,16 +204,14 @@ int moe_linear(const bitmoe_rows *x, const bitmoe_experts *w, const void *bias, 
     GemmArgs g = rows_product(x, w, nullptr, T, y, false);
     g.act = act;
     g.bias = bias;
-    g.bias_dtype = w->dtype;
     if (residual) {
         g.res = residual->data;
         g.ld_res = residual->ld;
-        g.res_dtype = residual->dtype;
+        g.res_f32 = residual->dtype == BITMOE_F32;
     }
     if (pre) {
         g.pre = pre->data;
         g.ld_pre = pre->ld;
-        g.pre_dtype = pre->dtype;
     }
     if ((rc = check_ws(ws, ws_bytes, gemm_ws_bytes(kForward, g)))) return rc;
     return launch_gemm(kForward, w->dtype, g, ws, as_stream(stream));

@@ -12,7 +12,8 @@ struct GemmRows {
     const void *p;
     const int32_t *map;
     int64_t ld;
-    int32_t rows, div;
+    int32_t rows;
+    uint32_t mul, shift;       // x / div = (x * mul >> 32) >> shift; mul 0: div 1
 };
 
 // C[m][n] = sum_k A[m][k] B[n][k] over the groups of rows that `offsets`
@@ -31,14 +32,14 @@ struct GemmArgs {
     int32_t E, R;
     int32_t M, N, K;           // M: kGradWeights only (elsewhere the group's rows);
                                // K: not kGradWeights (there the group's rows)
-    int32_t c_dtype;
-    int32_t accumulate;        // kGradWeights: add to what is there
+    bool c_f32;
+    bool accumulate;          // kGradWeights: add to what is there
     // epilogue: C = act(sum + bias) + res, the value before act kept in pre
     int32_t act;
     const void *bias, *res;
     void *pre;
     int64_t ld_res, ld_pre;
-    int32_t bias_dtype, res_dtype, pre_dtype;
+    bool res_f32;              // (bias and pre are of the operands' type)
 };
 
 // workspace of a product: a rule on the host-known sizes (E, R, M, N, K)

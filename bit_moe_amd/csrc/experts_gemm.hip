@@ -5,7 +5,7 @@
 // k_gemm: rows of any alignment.  A workgroup of 4 waves makes a 128 x 128
 // tile (64 x 64 a wave); a stage of 64 of the contraction is loaded into
 // registers while the one before it is multiplied out of LDS.
-#include "gemm_util.h"
+#include "gemm_tile.h"
 
 namespace {
 
@@ -30,8 +30,11 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     constexpr int NT = 64 * WM * WN, PA = BM * kBK / 8 / NT, PB = BN * kBK / 8 / NT;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr bool AKC = LAY != kGradWeights, BKC = LAY == kForward;
-    __shared__ __attribute__((aligned(16))) uint16_t sa[BM * kBK];
-    __shared__ __attribute__((aligned(16))) uint16_t sb[BN * kBK];
+    // the stage, and after it the epilogue's rows (32 of BN / WN + 4 floats a wave)
+    __shared__ __attribute__((aligned(16))) uint16_t lds[WM * WN * 32 * (BN / WN + 4) * 2];
+    static_assert(sizeof(lds) >= (BM + BN) * kBK * 2, "");
+    __shared__ int srow[BM];
+    uint16_t *sa = lds, *sb = lds + BM * kBK;
     Tile t;
     if (LAY == kGradWeights ? !find_tile_dw(g, mtiles, ntiles, blockIdx.x, &t)
                             : !find_tile<BM>(g, ntiles, blockIdx.x, &t))
@@ -87,6 +90,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
             }
         }
     };
+    set_rows<LAY, BM>(g, t, m0, tid, srow);
     f32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; i++)
@@ -115,35 +119,52 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
         }
         __syncthreads();
     }
-    const int mend = LAY == kGradWeights ? g.M : t.r1 - t.r0;
-#pragma unroll
-    for (int i = 0; i < TM; i++) {
-        const int m = m0 + wm * (BM / WM) + 16 * i + (lane & 15);
-        if (m >= mend) continue;
-#pragma unroll
-        for (int j = 0; j < TN; j++) {
-            float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            finish4<LAY>(g, t.e, LAY == kGradWeights ? m : t.r0 + m, n0 + wn * (BN / WN) + 16 * j + 4 * (lane >> 4), v);
-        }
-    }
+    __syncthreads();         // (srow, where the loop did not run)
+    tile_epilogue<LAY, DT, TM, TN>(g, acc, reinterpret_cast<float *>(lds), srow + wm * (BM / WM), t.e,
+                                   n0 + wn * (BN / WN), wave, lane);
+}
+
+// rows that all begin on 16-byte addresses, whole 8-element pieces
+bool on16(const void *p, int64_t ld, int cols) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && cols % 8 == 0;
+}
+template <int LAY>
+bool pieces_whole(const GemmArgs &g) {
+    if (LAY == kGradWeights) return on16(g.a.p, g.a.ld, g.M) && on16(g.b.p, g.b.ld, g.N);
+    return on16(g.a.p, g.a.ld, g.K) && on16(g.b.p, g.b.ld, LAY == kForward ? g.K : g.N) &&
+           (g.E == 1 || g.b_stride % 8 == 0);
+}
+
+template <int LAY, int BM, int BN>
+int64_t tiles(const GemmArgs &g, int *mt, int *nt) {
+    *nt = (g.N + BN - 1) / BN;
+    // (rows: the tiles of all groups, at most)
+    *mt = LAY == kGradWeights ? (g.M + BM - 1) / BM : g.R / BM + (g.E < g.R ? g.E : g.R);
+    const int64_t items = (LAY == kGradWeights ? g.E : 1) * (int64_t)*mt * *nt;
+    return (items + 7) / 8 * 8;
+}
+
+template <int LAY, int DT, int BM, int BN, int WM, int WN>
+int launch_tile(const GemmArgs &g, hipStream_t s) {
+    int mt, nt;
+    const int64_t grid = tiles<LAY, BM, BN>(g, &mt, &nt);
+    if (grid * 64 * WM * WN >= (int64_t)1 << 32) return BITMOE_EUNSUPPORTED;
+    constexpr int lds = 2 * (BM + BN) * kBK * 2 + BM * 4;
+    // (LDS above 64 KiB must be opted into per kernel and device)
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(k_gemm_tile<LAY, DT, BM, BN, WM, WN>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    k_gemm_tile<LAY, DT, BM, BN, WM, WN><<<(int)grid, 64 * WM * WN, lds, s>>>(g, mt, nt);
+    BM_LAUNCH_CHECK();
+    return BITMOE_OK;
 }
 
 template <int LAY, int DT>
 int launch_one(const GemmArgs &g, hipStream_t s) {
-    constexpr int BM = 128, BN = 128;
-    const int64_t nt = (g.N + BN - 1) / BN;
-    int64_t mt, items;
-    if (LAY == kGradWeights) {
-        mt = (g.M + BM - 1) / BM;
-        items = g.E * mt * nt;
-    } else {
-        // row tiles of all groups, at most
-        mt = g.R / BM + (g.E < g.R ? g.E : g.R);
-        items = mt * nt;
-    }
-    const int64_t grid = (items + 7) / 8 * 8;
+    if (pieces_whole<LAY>(g)) return launch_tile<LAY, DT, 256, 256, 2, 4>(g, s);
+    int mt, nt;
+    const int64_t grid = tiles<LAY, 128, 128>(g, &mt, &nt);
     if (grid * 256 >= (int64_t)1 << 32) return BITMOE_EUNSUPPORTED;
-    k_gemm<LAY, DT, BM, BN, 2, 2><<<(int)grid, 256, 0, s>>>(g, (int)mt, (int)nt);
+    k_gemm<LAY, DT, 128, 128, 2, 2><<<(int)grid, 256, 0, s>>>(g, mt, nt);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }

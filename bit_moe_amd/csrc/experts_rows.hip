@@ -39,11 +39,11 @@ __global__ void __launch_bounds__(256)
 k_swiglu(Mat gate, Mat up, Mat h, int R, int I, int cshift) {
     BM_FOR_PIECES(r, c, R, I, cshift) {
         float a[8], b[8];
-        load8(gate.p, (int64_t)r * gate.ld + c, I - c, DT, a);
-        load8(up.p, (int64_t)r * up.ld + c, I - c, DT, b);
+        load8<DT>(gate.p, (int64_t)r * gate.ld + c, I - c, false, a);
+        load8<DT>(up.p, (int64_t)r * up.ld + c, I - c, false, b);
 #pragma unroll
         for (int j = 0; j < 8; j++) a[j] = silu(a[j]) * b[j];
-        store8(h.p, (int64_t)r * h.ld + c, I - c, DT, a);
+        store8<DT>(h.p, (int64_t)r * h.ld + c, I - c, false, a);
     }
 }
 
@@ -53,17 +53,17 @@ __global__ void __launch_bounds__(256)
 k_swiglu_backward(Mat dh, Mat gate, Mat up, Mat dgate, Mat dup, int R, int I, int cshift) {
     BM_FOR_PIECES(r, c, R, I, cshift) {
         float d[8], a[8], b[8];
-        load8(dh.p, (int64_t)r * dh.ld + c, I - c, DT, d);
-        load8(gate.p, (int64_t)r * gate.ld + c, I - c, DT, a);
-        load8(up.p, (int64_t)r * up.ld + c, I - c, DT, b);
+        load8<DT>(dh.p, (int64_t)r * dh.ld + c, I - c, false, d);
+        load8<DT>(gate.p, (int64_t)r * gate.ld + c, I - c, false, a);
+        load8<DT>(up.p, (int64_t)r * up.ld + c, I - c, false, b);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const float p = 1.f / (1.f + __expf(-a[j])), g = a[j];
             a[j] = d[j] * b[j] * p * (1.f + g * (1.f - p));
             b[j] = d[j] * g * p;
         }
-        store8(dgate.p, (int64_t)r * dgate.ld + c, I - c, DT, a);
-        store8(dup.p, (int64_t)r * dup.ld + c, I - c, DT, b);
+        store8<DT>(dgate.p, (int64_t)r * dgate.ld + c, I - c, false, a);
+        store8<DT>(dup.p, (int64_t)r * dup.ld + c, I - c, false, b);
     }
 }
 
@@ -71,12 +71,12 @@ k_swiglu_backward(Mat dh, Mat gate, Mat up, Mat dgate, Mat dup, int R, int I, in
 // loaded together
 template <int DT, int KM>
 __global__ void __launch_bounds__(256)
-k_combine(Mat o, const float *w, int T, int k, int H, Mat res, int res_dtype, Mat y, int y_dtype, int cshift) {
+k_combine(Mat o, const float *w, int T, int k, int H, Mat res, bool res_f32, Mat y, bool y_f32, int cshift) {
     BM_FOR_PIECES(t, c, T, H, cshift) {
         float v[KM][8], acc[8];
 #pragma unroll
         for (int j = 0; j < KM; j++)
-            if (j < k) load8(o.p, ((int64_t)t * k + j) * o.ld + c, H - c, DT, v[j]);
+            if (j < k) load8<DT>(o.p, ((int64_t)t * k + j) * o.ld + c, H - c, false, v[j]);
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[i] = 0.f;
 #pragma unroll
@@ -88,11 +88,11 @@ k_combine(Mat o, const float *w, int T, int k, int H, Mat res, int res_dtype, Ma
             }
         if (res.p) {
             float q[8];
-            load8(res.p, (int64_t)t * res.ld + c, H - c, res_dtype, q);
+            load8<DT>(res.p, (int64_t)t * res.ld + c, H - c, res_f32, q);
 #pragma unroll
             for (int i = 0; i < 8; i++) acc[i] += q[i];
         }
-        store8(y.p, (int64_t)t * y.ld + c, H - c, y_dtype, acc);
+        store8<DT>(y.p, (int64_t)t * y.ld + c, H - c, y_f32, acc);
     }
 }
 
@@ -101,7 +101,7 @@ k_combine(Mat o, const float *w, int T, int k, int H, Mat res, int res_dtype, Ma
 // by a tree, the waves in order.
 template <int DT, int KM>
 __global__ void __launch_bounds__(256)
-k_combine_backward(Mat dy, int dy_dtype, Mat o, const float *w, int T, int k, int H, Mat d_o, float *dw) {
+k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int T, int k, int H, Mat d_o, float *dw) {
     __shared__ float part[KM][4];
     const int t = blockIdx.x, tid = threadIdx.x, nw = blockDim.x >> 6;
     float wt[KM], dot[KM];
@@ -112,11 +112,11 @@ k_combine_backward(Mat dy, int dy_dtype, Mat o, const float *w, int T, int k, in
     }
     for (int c = tid * 8; c < H; c += blockDim.x * 8) {
         float d[8], v[KM][8];
-        load8(dy.p, (int64_t)t * dy.ld + c, H - c, dy_dtype, d);
+        load8<DT>(dy.p, (int64_t)t * dy.ld + c, H - c, dy_f32, d);
         if (dw) {
 #pragma unroll
             for (int j = 0; j < KM; j++)
-                if (j < k) load8(o.p, ((int64_t)t * k + j) * o.ld + c, H - c, DT, v[j]);
+                if (j < k) load8<DT>(o.p, ((int64_t)t * k + j) * o.ld + c, H - c, false, v[j]);
 #pragma unroll
             for (int j = 0; j < KM; j++)
                 if (j < k)
@@ -130,7 +130,7 @@ k_combine_backward(Mat dy, int dy_dtype, Mat o, const float *w, int T, int k, in
                     float q[8];
 #pragma unroll
                     for (int i = 0; i < 8; i++) q[i] = wt[j] * d[i];
-                    store8(d_o.p, ((int64_t)t * k + j) * d_o.ld + c, H - c, DT, q);
+                    store8<DT>(d_o.p, ((int64_t)t * k + j) * d_o.ld + c, H - c, false, q);
                 }
         }
     }
@@ -161,14 +161,14 @@ k_act_backward(bm_host::ActBackward p, int rows_per, int want_sum) {
     if (c < p.N)
         for (int r = r0 + ty; r < r1; r += 8) {
             float d[8];
-            load8(p.dy, (int64_t)r * p.ld_dy + c, p.N - c, DT, d);
+            load8<DT>(p.dy, (int64_t)r * p.ld_dy + c, p.N - c, false, d);
             if (p.pre) {
                 float z[8];
-                load8(p.pre, (int64_t)r * p.ld_pre + c, p.N - c, DT, z);
+                load8<DT>(p.pre, (int64_t)r * p.ld_pre + c, p.N - c, false, z);
 #pragma unroll
                 for (int j = 0; j < 8; j++) d[j] *= act_slope(z[j], p.act);
             }
-            if (p.dz) store8(p.dz, (int64_t)r * p.ld_dz + c, p.N - c, DT, d);
+            if (p.dz) store8<DT>(p.dz, (int64_t)r * p.ld_dz + c, p.N - c, false, d);
 #pragma unroll
             for (int j = 0; j < 8; j++) sum[j] += d[j];
         }
@@ -199,7 +199,8 @@ k_bias_grad(const float *partial, int slices, int N, void *db, int db_dtype) {
 #pragma unroll
         for (int i = 0; i < 16; i++) s += red[i][tx];
         if (db_dtype == BITMOE_F32) static_cast<float *>(db)[c] = s;
-        else static_cast<uint16_t *>(db)[c] = (uint16_t)elem_bits(s, db_dtype);
+        else static_cast<uint16_t *>(db)[c] = (uint16_t)(db_dtype == BITMOE_BF16 ? elem_pair<BITMOE_BF16>(s, 0.f)
+                                                                              : elem_pair<BITMOE_F16>(s, 0.f));
     }
 }
 
@@ -209,11 +210,11 @@ template <int KM>
 int combine_k(const bitmoe_rows &o, const float *w, int T, int k, const bitmoe_rows *res, const bitmoe_rows &y,
               hipStream_t s) {
     const Grid2 g = pieces_grid(T, o.cols);
-    const int rt = res ? res->dtype : 0;
+    const bool rt = res && res->dtype == BITMOE_F32, yt = y.dtype == BITMOE_F32;
     if (o.dtype == BITMOE_BF16)
-        k_combine<BITMOE_BF16, KM><<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(res), rt, mat(&y), y.dtype, g.cshift);
+        k_combine<BITMOE_BF16, KM><<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(res), rt, mat(&y), yt, g.cshift);
     else
-        k_combine<BITMOE_F16, KM><<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(res), rt, mat(&y), y.dtype, g.cshift);
+        k_combine<BITMOE_F16, KM><<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(res), rt, mat(&y), yt, g.cshift);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }
@@ -222,9 +223,9 @@ int combine_backward_k(const bitmoe_rows &dy, const bitmoe_rows *o, const float 
                        const bitmoe_rows *d_o, float *dw, int dtype, hipStream_t s) {
     const int block = dy.cols <= 512 ? 64 : 256;
     if (dtype == BITMOE_BF16)
-        k_combine_backward<BITMOE_BF16, KM><<<T, block, 0, s>>>(mat(&dy), dy.dtype, mat(o), w, T, k, dy.cols, mat(d_o), dw);
+        k_combine_backward<BITMOE_BF16, KM><<<T, block, 0, s>>>(mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, T, k, dy.cols, mat(d_o), dw);
     else
-        k_combine_backward<BITMOE_F16, KM><<<T, block, 0, s>>>(mat(&dy), dy.dtype, mat(o), w, T, k, dy.cols, mat(d_o), dw);
+        k_combine_backward<BITMOE_F16, KM><<<T, block, 0, s>>>(mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, T, k, dy.cols, mat(d_o), dw);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }

@@ -32,13 +32,21 @@ BM_DEV f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
                                                       0, 0, 0);
 }
-BM_DEV float elem_f32(uint32_t bits, int dtype) { return dtype == BITMOE_BF16 ? bf16_to_f32(bits) : fp16_to_f32(bits); }
-BM_DEV uint32_t elem_bits(float v, int dtype) { return dtype == BITMOE_BF16 ? f32_to_bf16_rne(v) : f16_bits(v); }
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+template <int DT>
+BM_DEV float elem_f32(uint32_t bits) { return DT == BITMOE_BF16 ? bf16_to_f32(bits) : fp16_to_f32(bits); }
+// two values rounded to nearest, the first in the low half
+template <int DT>
+BM_DEV uint32_t elem_pair(float a, float b) {
+    if constexpr (DT == BITMOE_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2_t));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2_t));
+}
 
-// 16, 8 and 4 bytes at any element's address: gfx950 reads and writes global
+// 16 bytes at any element's address: gfx950 reads and writes global
 // memory at any alignment, so rows need not be aligned to a vector
 struct __attribute__((packed, aligned(2))) U128 { uint32_t w[4]; };
-struct __attribute__((packed, aligned(2))) U64 { uint32_t w[2]; };
 struct __attribute__((packed, aligned(4))) F128 { float w[4]; };
 
 BM_DEV uint4 load16(const uint16_t *p) {
@@ -54,87 +62,69 @@ BM_DEV uint4 load16_part(const uint16_t *p, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// four consecutive values of a row, the first n of them (n >= 1)
-BM_DEV void load4(const void *p, int64_t i, int n, int dtype, float *v) {
-    if (dtype == BITMOE_F32) {
+// eight consecutive values of a row of DT or fp32, the first n of them (n >= 1;
+// the rest 0)
+BM_DEV void load4_f32(const float *q, int n, float *v) {
+    if (n >= 4) {
+        const F128 u = *reinterpret_cast<const F128 *>(q);
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = u.w[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = j < n ? q[j] : 0.f;
+    }
+}
+template <int DT>
+BM_DEV void load8(const void *p, int64_t i, int n, bool f32, float *v) {
+    if (f32) {
         const float *q = static_cast<const float *>(p) + i;
-        if (n >= 4) {
-            const F128 u = *reinterpret_cast<const F128 *>(q);
-#pragma unroll
-            for (int j = 0; j < 4; j++) v[j] = u.w[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; j++) v[j] = j < n ? q[j] : 0.f;
-        }
-        return;
-    }
-    const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-    if (n >= 4) {
-        const U64 u = *reinterpret_cast<const U64 *>(q);
-#pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = elem_f32(u.w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, dtype);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = j < n ? elem_f32(q[j], dtype) : 0.f;
-    }
-}
-BM_DEV void store4(void *p, int64_t i, int n, int dtype, const float *v) {
-    if (dtype == BITMOE_F32) {
-        float *q = static_cast<float *>(p) + i;
-        if (n >= 4) {
-            *reinterpret_cast<F128 *>(q) = F128{{v[0], v[1], v[2], v[3]}};
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (j < n) q[j] = v[j];
-        }
-        return;
-    }
-    uint16_t *q = static_cast<uint16_t *>(p) + i;
-    if (n >= 4) {
-        *reinterpret_cast<U64 *>(q) = U64{{elem_bits(v[0], dtype) | elem_bits(v[1], dtype) << 16,
-                                           elem_bits(v[2], dtype) | elem_bits(v[3], dtype) << 16}};
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (j < n) q[j] = (uint16_t)elem_bits(v[j], dtype);
-    }
-}
-
-// eight consecutive values of a row, the first n of them (n >= 1; the rest 0)
-BM_DEV void load8(const void *p, int64_t i, int n, int dtype, float *v) {
-    if (dtype == BITMOE_F32) {
-        load4(p, i, n, dtype, v);
-        if (n > 4) load4(p, i + 4, n - 4, dtype, v + 4);
-        else v[4] = v[5] = v[6] = v[7] = 0.f;
+        load4_f32(q, n, v);
+        load4_f32(q + 4, n - 4, v + 4);
         return;
     }
     const uint16_t *q = static_cast<const uint16_t *>(p) + i;
     const uint4 u = n >= 8 ? load16(q) : load16_part(q, n);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = elem_f32(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu, dtype);
+    for (int j = 0; j < 8; j++) v[j] = elem_f32<DT>(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu);
 }
-BM_DEV void store8(void *p, int64_t i, int n, int dtype, const float *v) {
-    if (dtype != BITMOE_F32 && n >= 8) {
-        U128 u;
+template <int DT>
+BM_DEV void store8(void *p, int64_t i, int n, bool f32, const float *v) {
+    if (f32) {
+        float *q = static_cast<float *>(p) + i;
+        if (n >= 8) {
+            *reinterpret_cast<F128 *>(q) = F128{{v[0], v[1], v[2], v[3]}};
+            *reinterpret_cast<F128 *>(q + 4) = F128{{v[4], v[5], v[6], v[7]}};
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++) u.w[j] = elem_bits(v[2 * j], dtype) | elem_bits(v[2 * j + 1], dtype) << 16;
-        *reinterpret_cast<U128 *>(static_cast<uint16_t *>(p) + i) = u;
+            for (int j = 0; j < 8; j++)
+                if (j < n) q[j] = v[j];
+        }
         return;
     }
-    store4(p, i, n, dtype, v);
-    if (n > 4) store4(p, i + 4, n - 4, dtype, v + 4);
+    uint16_t *q = static_cast<uint16_t *>(p) + i;
+    U128 u;
+#pragma unroll
+    for (int j = 0; j < 4; j++) u.w[j] = elem_pair<DT>(v[2 * j], v[2 * j + 1]);
+    if (n >= 8) {
+        *reinterpret_cast<U128 *>(q) = u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < n) q[j] = (uint16_t)(u.w[j >> 1] >> (16 * (j & 1)));
+    }
 }
 
 // ---- rows and groups ------------------------------------------------------
+// m / div for 0 <= m < 2^31 (the multiplier and shift of rows_arg)
+BM_DEV int divided(const GemmRows &q, int m) { return q.mul ? (int)(__umulhi((uint32_t)m, q.mul) >> q.shift) : m; }
 // matrix row of the call's row r, or -1
 BM_DEV int row_of(const GemmRows &q, int r) {
     int m = r;
     if (q.map) {
         m = q.map[r];
         if (m < 0) return -1;
-        if (q.div > 1) m = (int)((uint32_t)m / (uint32_t)q.div);
+        m = divided(q, m);
     }
     return m < q.rows ? m : -1;
 }
@@ -291,43 +281,83 @@ BM_DEV float act_slope(float z, int act) {
     }
 }
 
-// four outputs (m fixed, n.. n+3) of a tile
-template <int LAY>
-BM_DEV void finish4(const GemmArgs &g, int e, int m, int n, float *v) {
+// eight outputs of a row: n.. of row `row` of the output
+template <int LAY, int DT>
+BM_DEV void finish8(const GemmArgs &g, int e, int row, int n, float *v) {
     const int left = g.N - n;
-    if (left <= 0) return;
+    if (left <= 0 || row < 0) return;
+    int64_t at = (int64_t)row * g.c.ld + n;
     if constexpr (LAY == kGradWeights) {
-        const int64_t at = (int64_t)e * g.c_stride + (int64_t)m * g.c.ld + n;
+        at += (int64_t)e * g.c_stride;
         if (g.accumulate) {
-            float o[4];
-            load4(g.c.p, at, left, g.c_dtype, o);
+            float o[8];
+            load8<DT>(g.c.p, at, left, g.c_f32, o);
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[j] += o[j];
+            for (int j = 0; j < 8; j++) v[j] += o[j];
         }
-        store4(const_cast<void *>(g.c.p), at, left, g.c_dtype, v);
-    } else {
-        const int row = row_of(g.c, m);
-        if (row < 0) return;
-        if constexpr (LAY == kForward) {
-            if (g.bias) {
-                float o[4];
-                load4(g.bias, n, left, g.bias_dtype, o);
+    }
+    if constexpr (LAY == kForward) {
+        if (g.bias) {
+            float o[8];
+            load8<DT>(g.bias, n, left, false, o);
 #pragma unroll
-                for (int j = 0; j < 4; j++) v[j] += o[j];
-            }
-            if (g.pre) store4(g.pre, (int64_t)row * g.ld_pre + n, left, g.pre_dtype, v);
-            if (g.act != BITMOE_ACT_NONE) {
-#pragma unroll
-                for (int j = 0; j < 4; j++) v[j] = act_fwd(v[j], g.act);
-            }
-            if (g.res) {
-                float o[4];
-                load4(g.res, (int64_t)row * g.ld_res + n, left, g.res_dtype, o);
-#pragma unroll
-                for (int j = 0; j < 4; j++) v[j] += o[j];
-            }
+            for (int j = 0; j < 8; j++) v[j] += o[j];
         }
-        store4(const_cast<void *>(g.c.p), (int64_t)row * g.c.ld + n, left, g.c_dtype, v);
+        if (g.pre) store8<DT>(g.pre, (int64_t)row * g.ld_pre + n, left, false, v);
+        if (g.act != BITMOE_ACT_NONE) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = act_fwd(v[j], g.act);
+        }
+        if (g.res) {
+            float o[8];
+            load8<DT>(g.res, (int64_t)row * g.ld_res + n, left, g.res_f32, o);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] += o[j];
+        }
+    }
+    store8<DT>(const_cast<void *>(g.c.p), at, left, g.c_f32, v);
+}
+
+// the output row of each of a tile's rows, or -1
+template <int LAY, int BM>
+BM_DEV void set_rows(const GemmArgs &g, const Tile &t, int m0, int tid, int *srow) {
+    if (tid < BM) {
+        const int m = m0 + tid;
+        srow[tid] = LAY == kGradWeights ? (m < g.M ? m : -1) : m < t.r1 - t.r0 ? row_of(g.c, t.r0 + m) : -1;
+    }
+}
+
+// The waves' accumulators to memory.  A lane holds 4 columns of one row of
+// each 16 x 16 product; through LDS (a wave's own part of `lds`, 32 rows at a
+// time) it takes 8 columns, so that 8 lanes (EW 64) write a whole 128-byte
+// line.  The pass over the wave's rows is a loop whose end moves the
+// accumulators down: one copy of the code, and no accumulator is indexed.
+// srow: the output row of each of the tile's rows, or -1.
+template <int LAY, int DT, int TM, int TN>
+BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, const int *srow, int e, int n0,
+                          int wave, int lane) {
+    constexpr int QI = 2, EW = 16 * TN, LDW = EW + 4, LPR = EW / 8, RPI = 64 / LPR;
+    static_assert(TM % QI == 0, "");
+    float *sw = lds + wave * (16 * QI * LDW);
+#pragma unroll 1
+    for (int q = 0; q < TM; q += QI) {
+#pragma unroll
+        for (int ii = 0; ii < QI; ii++)
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+                *reinterpret_cast<f32x4 *>(sw + (16 * ii + (lane & 15)) * LDW + 16 * j + 4 * (lane >> 4)) = acc[ii][j];
+#pragma unroll
+        for (int it = 0; it < 16 * QI / RPI; it++) {
+            const int r = it * RPI + lane / LPR, c = (lane % LPR) * 8;
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
+            float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            finish8<LAY, DT>(g, e, srow[16 * q + r], n0 + c, v);
+        }
+#pragma unroll
+        for (int ii = 0; ii + QI < TM; ii++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) acc[ii][j] = acc[ii + QI][j];
     }
 }
 
