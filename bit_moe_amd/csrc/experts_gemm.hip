@@ -11,6 +11,8 @@ namespace {
 
 using namespace bm;
 
+constexpr int kBK = 64;             // contraction per stage
+
 // 8 elements of an operand's stage: row `row` of the rows it runs along
 // (KC: an output row, KS: a step of the contraction), elements c8.. of it
 struct Piece {
@@ -52,7 +54,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     int ar[PA], ac[PA], br[PB], bc[PB];
 #pragma unroll
     for (int i = 0; i < PA; i++) {
-        piece_at<AKC, BM>(tid + i * NT, &ar[i], &ac[i]);
+        piece_at<AKC, BM, kBK>(tid + i * NT, &ar[i], &ac[i]);
         arow[i] = nullptr;
         if (AKC) {
             const int r = t.r0 + m0 + ar[i];
@@ -62,7 +64,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     }
 #pragma unroll
     for (int i = 0; i < PB; i++) {
-        piece_at<BKC, BN>(tid + i * NT, &br[i], &bc[i]);
+        piece_at<BKC, BN, kBK>(tid + i * NT, &br[i], &bc[i]);
         brow[i] = nullptr;
         if (BKC && n0 + br[i] < g.N) brow[i] = B + (int64_t)(n0 + br[i]) * g.b.ld;
     }
@@ -108,9 +110,9 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
         for (int kk = 0; kk < kBK; kk += 32) {
             s16x8 fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i++) fa[i] = frag<AKC, BM>(sa, wm * (BM / WM) + 16 * i, kk, lane);
+            for (int i = 0; i < TM; i++) fa[i] = frag<AKC, BM, kBK>(sa, wm * (BM / WM) + 16 * i, kk, lane);
 #pragma unroll
-            for (int j = 0; j < TN; j++) fb[j] = frag<BKC, BN>(sb, wn * (BN / WN) + 16 * j, kk, lane);
+            for (int j = 0; j < TN; j++) fb[j] = frag<BKC, BN, kBK>(sb, wn * (BN / WN) + 16 * j, kk, lane);
             // (B first: a lane then holds four consecutive columns of one row)
 #pragma unroll
             for (int i = 0; i < TM; i++)
@@ -149,7 +151,7 @@ int launch_tile(const GemmArgs &g, hipStream_t s) {
     int mt, nt;
     const int64_t grid = tiles<LAY, BM, BN>(g, &mt, &nt);
     if (grid * 64 * WM * WN >= (int64_t)1 << 32) return BITMOE_EUNSUPPORTED;
-    constexpr int lds = 2 * (BM + BN) * kBK * 2 + BM * 4;
+    constexpr int lds = TileLds<LAY, BM, BN, WM, WN>::bytes;
     // (LDS above 64 KiB must be opted into per kernel and device)
     (void)hipFuncSetAttribute(reinterpret_cast<const void *>(k_gemm_tile<LAY, DT, BM, BN, WM, WN>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);

@@ -19,8 +19,6 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kBK = 64;             // contraction per stage
-
 // ---- elements -------------------------------------------------------------
 // DT: BITMOE_BF16 or BITMOE_F16
 template <int DT>
@@ -202,24 +200,30 @@ BM_DEV bool find_tile_dw(const GemmArgs &g, int mt, int nt, int bid, Tile *t) {
 }
 
 // ---- tiles in LDS ---------------------------------------------------------
-// An operand's stage is X rows of kBK elements (contiguous along the
-// contraction: KC) or kBK rows of X elements (KS), in 16-byte pieces.
-//  KC: piece c of row r at slot c ^ (r & 7) of the row's 8: the 16-byte reads
-//      of 8 consecutive rows, one piece each, fall on different banks.
+// An operand's stage is X rows of BK elements (contiguous along the
+// contraction: KC) or BK rows of X elements (KS), in 16-byte pieces.
+//  KC: piece c of row r at slot c ^ swz(r) of the row's pieces, so that the
+//      16-byte reads of consecutive rows, one piece each, run without bank
+//      conflicts (measured: 4.3 cycles for a wave's 1 KiB; (r >> 2) & 3 or
+//      padded rows of 64 + 16 bytes take 8.1, unswizzled rows of 128 16.2).
 //  KS: pieces move in pairs of 32 bytes, pair c of row k at c ^ swz(k): a
 //      transposed read takes 32 bytes of each of 4 consecutive rows (8, 16, 24
 //      rows further for the wave's other lanes), and these fall on different
 //      banks too.
+template <int BK>
+BM_DEV int kc_swz(int r) {
+    return BK == 64 ? r & 7 : (r >> 1) & 3;
+}
 template <int X>
 BM_DEV int ks_swz(int k) {
     return X >= 128 ? (k & 3) | ((k >> 1) & 4) : (k & 3);
 }
 // piece p of the stage (in LDS order): its row and its piece in the row
-template <bool KC, int X>
+template <bool KC, int X, int BK>
 BM_DEV void piece_at(int p, int *row, int *col) {
     if (KC) {
-        *row = p >> 3;
-        *col = (p & 7) ^ (*row & 7);
+        *row = p / (BK / 8);
+        *col = p % (BK / 8) ^ kc_swz<BK>(*row);
     } else {
         *row = p / (X / 8);
         const int s = p % (X / 8);
@@ -228,12 +232,12 @@ BM_DEV void piece_at(int p, int *row, int *col) {
 }
 // the wave's matrix-core operand: 16 rows (KC) or columns (KS) from x0, 32 of
 // the contraction from kk; lane l holds row l % 16, contraction 8 (l / 16) + j
-template <bool KC, int X>
+template <bool KC, int X, int BK>
 BM_DEV s16x8 frag(const uint16_t *tile, int x0, int kk, int lane) {
     const int i = lane & 15, q = lane >> 4;
     if (KC) {
         const int row = x0 + i;
-        return *reinterpret_cast<const s16x8 *>(tile + row * kBK + ((((kk >> 3) + q) ^ (row & 7)) << 3));
+        return *reinterpret_cast<const s16x8 *>(tile + row * BK + ((((kk >> 3) + q) ^ kc_swz<BK>(row)) << 3));
     } else {
         // a transposing read: 16 lanes give 4 rows of 16 elements, four lanes
         // a row, and receive the 16 columns, 4 elements each
@@ -241,8 +245,7 @@ BM_DEV s16x8 frag(const uint16_t *tile, int x0, int kk, int lane) {
         const int k = kk + 8 * q + (i >> 2);
         const uint16_t *p = tile + k * X + (((x0 >> 4) ^ ks_swz<X>(k)) << 4) + ((i & 3) << 2);
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4 *)(tile + (k + 4) * X + (((x0 >> 4) ^ ks_swz<X>(k + 4)) << 4) + ((i & 3) << 2)));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * X));
         return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     }
 }
