@@ -11,7 +11,6 @@ namespace {
 
 using namespace bm;
 
-constexpr int kBK = 64;             // contraction per stage
 
 // 8 elements of an operand's stage: row `row` of the rows it runs along
 // (KC: an output row, KS: a step of the contraction), elements c8.. of it
@@ -54,7 +53,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     int ar[PA], ac[PA], br[PB], bc[PB];
 #pragma unroll
     for (int i = 0; i < PA; i++) {
-        piece_at<AKC, BM, kBK>(tid + i * NT, &ar[i], &ac[i]);
+        piece_at<AKC, BM>(tid + i * NT, &ar[i], &ac[i]);
         arow[i] = nullptr;
         if (AKC) {
             const int r = t.r0 + m0 + ar[i];
@@ -64,7 +63,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     }
 #pragma unroll
     for (int i = 0; i < PB; i++) {
-        piece_at<BKC, BN, kBK>(tid + i * NT, &br[i], &bc[i]);
+        piece_at<BKC, BN>(tid + i * NT, &br[i], &bc[i]);
         brow[i] = nullptr;
         if (BKC && n0 + br[i] < g.N) brow[i] = B + (int64_t)(n0 + br[i]) * g.b.ld;
     }
@@ -110,9 +109,9 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
         for (int kk = 0; kk < kBK; kk += 32) {
             s16x8 fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i++) fa[i] = frag<AKC, BM, kBK>(sa, wm * (BM / WM) + 16 * i, kk, lane);
+            for (int i = 0; i < TM; i++) fa[i] = frag<AKC, BM>(sa, wm * (BM / WM) + 16 * i, kk, lane);
 #pragma unroll
-            for (int j = 0; j < TN; j++) fb[j] = frag<BKC, BN, kBK>(sb, wn * (BN / WN) + 16 * j, kk, lane);
+            for (int j = 0; j < TN; j++) fb[j] = frag<BKC, BN>(sb, wn * (BN / WN) + 16 * j, kk, lane);
             // (B first: a lane then holds four consecutive columns of one row)
 #pragma unroll
             for (int i = 0; i < TM; i++)
@@ -122,8 +121,8 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
         __syncthreads();
     }
     __syncthreads();         // (srow, where the loop did not run)
-    tile_epilogue<LAY, DT, TM, TN>(g, acc, reinterpret_cast<float *>(lds), srow + wm * (BM / WM), t.e,
-                                   n0 + wn * (BN / WN), wave, lane);
+    tile_epilogue<LAY, DT, BM, BN, 1>(g, acc, reinterpret_cast<float *>(lds), srow, t.e, n0, wm * (BM / WM),
+                                      wn * (BN / WN), wave, lane);
 }
 
 // rows that all begin on 16-byte addresses, whole 8-element pieces

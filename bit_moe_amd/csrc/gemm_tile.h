@@ -1,19 +1,27 @@
 // The matrix products for rows on 16-byte addresses.
 //
-// A stage is 32 of the contraction of a BM x BN tile, loaded from memory
-// straight into LDS (global_load_lds, 16 bytes a lane, no registers) in a ring
-// of four: when the matrix cores work on stage s, its operands are in
-// registers already, those of s + 1 are being read from LDS, and s + 2 .. s + 4
-// are on their way, so a load has three stages (3 x 1024 cycles at 256 x 256)
-// to arrive.  One barrier a stage.
+// A stage is 64 of the contraction of a BM x BN tile, loaded from memory
+// straight into LDS (global_load_lds, 16 bytes a lane, no registers), two
+// stages deep.  Each stage is four units, the halves A0, A1 of A's rows and B0,
+// B1 of B's, and is multiplied in four phases, a quadrant of the tile each
+// (every wave has its part of every quadrant):
+//   even stages  A0 B0,  A0 B1,  A1 B1,  A1 B0     (odd: B0 and B1 exchanged)
+// A phase reads from LDS what the next one needs and its registers do not
+// hold, so a unit is read once, at one known phase, and its place is free for
+// the stage after next long before that stage is due:
+//   phase            0            1            2            3
+//   reads            B second     A1           -            next A0, B first
+//   loads (stage+2)  A0           B first      B second     A1
+// A load has six phases to arrive.  Of the stage's four phases three begin
+// with a barrier.  Loads spread among the products this way because a CU takes
+// about 16 cycles for each; rows of 128 bytes because L2 serves 64-byte pieces
+// at half the rate (a ring of 32-wide stages ran 8192^3 at 1172 TFLOP/s, 1822
+// with its loads left out).
 #pragma once
 
 #include "gemm_util.h"
 
 namespace bm {
-
-constexpr int kTK = 32;             // contraction per stage
-constexpr int kRing = 4;
 
 // what a piece outside the operand reads
 __device__ const uint4 kZeroPiece = {0, 0, 0, 0};
@@ -23,7 +31,7 @@ BM_DEV uint32_t lds_addr(const void *p) {
 }
 // 16 (4) bytes per lane to LDS, lane l's at `lds` (one for the wave) + 16 l
 // (4 l).  In asm, because the compiler would wait for it before the next LDS
-// read, of whatever stage; ring_barrier() waits instead.
+// read, of whatever stage; phase_barrier() waits instead.
 BM_DEV void dma16(const void *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
 }
@@ -33,32 +41,64 @@ BM_DEV void dma4(const void *src, uint32_t lds) {
 // all but this wave's last N loads have arrived, its LDS reads are done, and
 // so for every wave of the workgroup
 template <int N>
-BM_DEV void ring_barrier() {
+BM_DEV void phase_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// dynamic LDS of a tile: the ring; the output rows; for the weights' gradient
-// each wave's ring of row maps (32 of A's, 32 of B's per stage).  The epilogue
-// takes the ring's place.
+// dynamic LDS of a tile: two stages; the output rows; for the weights'
+// gradient each wave's ring of row maps (64 of A's, 64 of B's, four stages).
+// The epilogue takes the stages' place.
 template <int LAY, int BM, int BN, int WM, int WN>
 struct TileLds {
-    static constexpr int ring = kRing * (BM + BN) * kTK * 2;
-    static constexpr int maps = ring + BM * 4;
-    static constexpr int bytes = maps + (LAY == kGradWeights ? WM * WN * 4 * 64 * 4 : 0);
-    static_assert(WM * WN * 32 * (BN / WN + 4) * 4 <= ring, "the epilogue's part");
+    static constexpr int rows = 2 * (BM + BN) * kBK * 2;
+    static constexpr int maps = rows + BM * 4;
+    static constexpr int bytes = maps + (LAY == kGradWeights ? WM * WN * 4 * 128 * 4 : 0);
+    static_assert(WM * WN * 32 * (BN / WN + 4) * 4 <= rows, "the epilogue's part");
     static_assert(bytes <= 160 * 1024, "");
 };
+
+// The matrix-core operands of a wave by address: `at` is the lane's place for
+// product 0 of the first half of a stage; the others follow by constants (an
+// exclusive or where the swizzle mixes with them), so that a unit's reads need
+// one register, and are made anew each stage for the same reason.
+template <bool KC, int X>
+BM_DEV uint32_t frag_place(uint32_t unit, int x0, int lane) {
+    const int i = lane & 15, q = lane >> 4;
+    if (KC) return unit + (x0 + i) * (kBK * 2) + ((q ^ kc_swz(i)) << 4);
+    const int k = 8 * q + (i >> 2);
+    return unit + k * (X * 2) + (((x0 >> 4) ^ ks_swz<X>(k)) << 5) + ((i & 3) << 3);
+}
+// product i (rows or columns 16 i.. of the wave's part, which is a multiple of
+// a power of two above i), half kk
+template <bool KC, int X>
+BM_DEV s16x8 frag_at(uint32_t at, int i, int kk) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (KC) {
+        typedef const __attribute__((address_space(3))) s16x8 lds_s16x8;
+        return *(lds_s16x8 *)((at ^ (uint32_t)(kk * 64)) + i * (16 * kBK * 2));
+    }
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const uint32_t p = (at ^ (uint32_t)(i * 32)) + kk * (32 * X * 2);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * X * 2));
+    return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#else
+    (void)at; (void)i; (void)kk;        // device code only; the host pass sees this body
+    return s16x8{};
+#endif
+}
 
 template <int LAY, int DT, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN)
 k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
-    constexpr int NW = WM * WN, PA = BM * kTK / 8 / (64 * NW), PB = BN * kTK / 8 / (64 * NW);
-    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int NW = WM * WN, UM = BM / 2, UN = BN / 2;                  // a unit's rows
+    constexpr int PA = UM * kBK / 8 / (64 * NW), PB = UN * kBK / 8 / (64 * NW);   // a unit's loads per wave
+    constexpr int TI = UM / WM / 16, TJ = UN / WN / 16;                    // 16 x 16 products of a wave in a quadrant
     constexpr bool AKC = LAY != kGradWeights, BKC = LAY == kForward;
-    constexpr int kStage = (BM + BN) * kTK;        // elements
-    constexpr int kLoads = PA + PB + (LAY == kGradWeights);
-    static_assert(PA >= 1 && PB >= 1, "");
-    extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+    constexpr bool kMaps = LAY == kGradWeights;
+    constexpr int kUA = UM * kBK, kUB = UN * kBK, kStage = 2 * (kUA + kUB);       // elements
+    static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW, "");
+    extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
     Tile t;
     if (LAY == kGradWeights ? !find_tile_dw(g, mtiles, ntiles, blockIdx.x, &t)
                             : !find_tile<BM>(g, ntiles, blockIdx.x, &t))
@@ -67,156 +107,209 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     const int wm = wave / WN, wn = wave % WN;
     const int m0 = t.m * BM, n0 = t.n * BN;
     const int kend = LAY == kGradWeights ? t.r1 - t.r0 : g.K;
-    const int stages = (kend + kTK - 1) / kTK;
+    const int stages = (kend + kBK - 1) / kBK;
     const uint16_t *A = static_cast<const uint16_t *>(g.a.p);
     const uint16_t *B = static_cast<const uint16_t *>(g.b.p);
     if (LAY != kGradWeights) B += (int64_t)t.e * g.b_stride;
     const uint16_t *zero = reinterpret_cast<const uint16_t *>(&kZeroPiece);
 
-    // Piece i of this thread in LDS order: tid + 64 NW i.  Its place in the
-    // row does not depend on i (the rows of successive pieces differ by a
-    // multiple of the swizzles' period), its row does.
+    // Piece i of this thread in a unit, in LDS order: tid + 64 NW i.  Its
+    // place in the row does not depend on i (the rows of successive pieces
+    // differ by a multiple of the swizzles' period), its row does.
     int ar, ac, br, bc;
-    piece_at<AKC, BM, kTK>(tid, &ar, &ac);
-    piece_at<BKC, BN, kTK>(tid, &br, &bc);
-    constexpr int kRowA = AKC ? 16 * NW : 64 * NW * 8 / BM, kRowB = BKC ? 16 * NW : 64 * NW * 8 / BN;
+    piece_at<AKC, UM>(tid, &ar, &ac);
+    piece_at<BKC, UN>(tid, &br, &bc);
+    constexpr int kRowA = AKC ? 8 * NW : 64 * NW * 8 / UM, kRowB = BKC ? 8 * NW : 64 * NW * 8 / UN;
     static_assert((kRowA % 16 == 0 || PA == 1) && (kRowB % 16 == 0 || PB == 1), "the swizzles' period");
-    // KC: each piece's address, and how far it moves per stage (0: the zero
-    // piece).  Rows past the group, and columns past the matrix, read its
-    // last row (their results are not stored).
-    const uint16_t *ap[PA], *bp[PB];
-    int astep[PA];
-    if (AKC) {
+    // KC: each piece's address in the first stage, and whether it is there.
+    // Rows past the group, and columns past the matrix, read its last row
+    // (their results are not stored).
+    const uint16_t *ap[2][PA], *bp[2][PB];
+    bool ais[2][PA];
 #pragma unroll
-        for (int i = 0; i < PA; i++) {
-            const int row = row_of(g.a, min(t.r0 + m0 + ar + i * kRowA, t.r1 - 1));
-            ap[i] = row >= 0 ? A + (int64_t)row * g.a.ld + 8 * ac : zero;
-            astep[i] = row >= 0 ? kTK : 0;
+    for (int h = 0; h < 2; h++) {
+        if (AKC) {
+#pragma unroll
+            for (int i = 0; i < PA; i++) {
+                const int row = row_of(g.a, min(t.r0 + m0 + h * UM + ar + i * kRowA, t.r1 - 1));
+                ais[h][i] = row >= 0;
+                ap[h][i] = A + (int64_t)max(row, 0) * g.a.ld + 8 * ac;
+            }
+        }
+        if (BKC) {
+#pragma unroll
+            for (int i = 0; i < PB; i++)
+                bp[h][i] = B + (int64_t)min(n0 + h * UN + br + i * kRowB, g.N - 1) * g.b.ld + 8 * bc;
         }
     }
-    if (BKC) {
+    // KS: the column within the matrix, per half
+    int acol[2], bcol[2];
 #pragma unroll
-        for (int i = 0; i < PB; i++) bp[i] = B + (int64_t)min(n0 + br + i * kRowB, g.N - 1) * g.b.ld + 8 * bc;
+    for (int h = 0; h < 2; h++) {
+        acol[h] = m0 + h * UM + 8 * ac < g.M ? m0 + h * UM + 8 * ac : 0;
+        bcol[h] = n0 + h * UN + 8 * bc < g.N ? n0 + h * UN + 8 * bc : 0;
     }
-    // KS: the column within the matrix
-    const int acol = m0 + 8 * ac < g.M ? m0 + 8 * ac : 0, bcol = n0 + 8 * bc < g.N ? n0 + 8 * bc : 0;
-    // the weights' gradient: the wave's own copy of the rows' maps, three stages
-    // ahead of the loads that go by them
-    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::maps) + wave * 256;
+    // The weights' gradient: the wave's own copy of the rows' maps, fetched two
+    // stages before the loads that go by them; a stage's rows are resolved at
+    // the operand's first unit and kept for its second.
+    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::maps) + wave * 512;
     const uint32_t maps_at = lds_addr(maps);
-    auto fetch_maps = [&](int s) {
-        const int32_t *m = lane < 32 ? g.a.map : g.b.map;
-        const int k = min(s * kTK + (lane & 31), kend - 1);
-        dma4(m ? static_cast<const void *>(m + t.r0 + k) : zero, maps_at + (s & 3) * 256);
+    auto fetch_map = [&](const GemmRows &q, int s, int b) {
+        const int k = min(s * kBK + lane, kend - 1);
+        dma4(q.map ? static_cast<const void *>(q.map + t.r0 + k) : zero, maps_at + ((s & 3) * 128 + b * 64) * 4);
     };
-    auto map_row = [&](const GemmRows &q, int at, int s, int k) {
-        if (k >= kend) return -1;
-        int m = t.r0 + k;
+    auto map_row = [&](const GemmRows &q, int b, int s, int k) {
+        if (s * kBK + k >= kend) return -1;
+        int m = t.r0 + s * kBK + k;
         if (q.map) {
-            m = maps[(s & 3) * 64 + at];
+            m = maps[(s & 3) * 128 + b * 64 + k];
             if (m < 0) return -1;
             m = divided(q, m);
         }
         return m < q.rows ? m : -1;
     };
+    const uint16_t *arow[PA], *brow[PB];
     const uint32_t lds0 = lds_addr(lds) + wave * 1024;
-    // load i of a stage (A's pieces, then B's, then the maps)
-    auto load_one = [&](int s, int i) {
-        const int k0 = s * kTK;
-        const uint32_t la = lds0 + (s & 3) * (kStage * 2), lb = la + BM * kTK * 2;
-        if (i < PA) {
-            const uint16_t *p;
-            if (AKC) {
-                p = k0 + 8 * ac < kend ? ap[i] : zero;
-                ap[i] += astep[i];
-            } else {
-                const int k = ar + i * kRowA, r = map_row(g.a, k, s, k0 + k);
-                p = r >= 0 ? A + (int64_t)r * g.a.ld + acol : zero;
-            }
-            dma16(p, la + i * (NW * 1024));
-        } else if (i < PA + PB) {
-            const uint16_t *p;
-            i -= PA;
-            if (BKC) {
-                p = k0 + 8 * bc < kend ? bp[i] : zero;
-                bp[i] += kTK;
-            } else {
-                const int k = br + i * kRowB;
-                const int r = LAY == kGradWeights ? map_row(g.b, 32 + k, s, k0 + k) : k0 + k < kend ? k0 + k : -1;
-                p = r >= 0 ? B + (int64_t)r * g.b.ld + bcol : zero;
-            }
-            dma16(p, lb + i * (NW * 1024));
+    // load i of A's (B's) half h of stage s
+    auto load_a = [&](int s, int buf, int h, int i) {
+        const uint16_t *p;
+        if (AKC) {
+            p = s * kBK + 8 * ac < kend && ais[h][i] ? ap[h][i] + s * kBK : zero;
         } else {
-            fetch_maps(s + 3);
+            p = arow[i] ? arow[i] + acol[h] : zero;
+        }
+        dma16(p, lds0 + (buf * kStage + h * kUA) * 2 + i * (NW * 1024));
+    };
+    auto load_b = [&](int s, int buf, int h, int i) {
+        const uint16_t *p;
+        if (BKC) {
+            p = s * kBK + 8 * bc < kend ? bp[h][i] + s * kBK : zero;
+        } else if (kMaps) {
+            p = brow[i] ? brow[i] + bcol[h] : zero;
+        } else {
+            const int k = s * kBK + br + i * kRowB;
+            p = k < kend ? B + (int64_t)k * g.b.ld + bcol[h] : zero;
+        }
+        dma16(p, lds0 + (buf * kStage + 2 * kUA + h * kUB) * 2 + i * (NW * 1024));
+    };
+    // what the unit of phase p of stage s needs before its loads
+    auto ready = [&](int s, int p) {
+        if (!kMaps || p > 1) return;
+        if (p == 0) {
+#pragma unroll
+            for (int i = 0; i < PA; i++) {
+                const int r = map_row(g.a, 0, s, ar + i * kRowA);
+                arow[i] = r >= 0 ? A + (int64_t)r * g.a.ld : nullptr;
+            }
+            fetch_map(g.a, s + 2, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PB; i++) {
+                const int r = map_row(g.b, 1, s, br + i * kRowB);
+                brow[i] = r >= 0 ? B + (int64_t)r * g.b.ld : nullptr;
+            }
+            fetch_map(g.b, s + 2, 1);
         }
     };
-    auto load = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < kLoads; i++) load_one(s, i);
+    // the loads of phase p for stage s, of parity f: its place in LDS, and B's
+    // half that comes first
+    auto load = [&](int s, int f, int p, int i) {
+        if (p == 0 || p == 3) {
+            if (i < PA) load_a(s, f, p == 3, i);
+        } else if (i < PB) {
+            load_b(s, f, p == 1 ? f : 1 - f, i);
+        }
     };
-    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::ring);
-    static_assert(BM <= 64 * NW, "");
+    constexpr int kLoads = PA > PB ? PA : PB;
+    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::rows);
     set_rows<LAY, BM>(g, t, m0, tid, srow);
-    f32x4 acc[TM][TN];
+
+    f32x4 acc[2 * TI][2 * TJ];
 #pragma unroll
-    for (int i = 0; i < TM; i++)
+    for (int i = 0; i < 2 * TI; i++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    s16x8 fa[2][TM], fb[2][TN];
-    auto read_a = [&](int s, int i) {
-        return frag<AKC, BM, kTK>(lds + (s & 3) * kStage, wm * (BM / WM) + 16 * i, 0, lane);
+        for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s16x8 ra0[2][TI], ra1[2][TI], rb0[2][TJ], rb1[2][TJ];       // [half of the stage's contraction]
+    static_assert((TI & (TI - 1)) == 0 && (TJ & (TJ - 1)) == 0 && kUA % 512 == 0 && kUB % 512 == 0, "frag_at");
+    uint32_t a_at = frag_place<AKC, UM>(lds_addr(lds), wm * (UM / WM), lane);
+    uint32_t b_at = frag_place<BKC, UN>(lds_addr(lds) + 4 * kUA, wn * (UN / WN), lane);
+    auto read_a = [&](int buf, int h, int kk, s16x8 (&r)[2][TI]) {
+#pragma unroll
+        for (int i = 0; i < TI; i++) r[kk][i] = frag_at<AKC, UM>(a_at + (buf * kStage + h * kUA) * 2, i, kk);
     };
-    auto read_b = [&](int s, int j) {
-        return frag<BKC, BN, kTK>(lds + (s & 3) * kStage + BM * kTK, wn * (BN / WN) + 16 * j, 0, lane);
+    auto read_b = [&](int buf, int h, int kk, s16x8 (&r)[2][TJ]) {
+#pragma unroll
+        for (int j = 0; j < TJ; j++) r[kk][j] = frag_at<BKC, UN>(b_at + (buf * kStage + h * kUB) * 2, j, kk);
     };
-    // Stage s's products, in parts, each with its share of the reads of s + 1
-    // before it and of the loads of s + 4 after it (into s's own place: its
-    // operands are in registers).  Issued together after the barrier, the 32
-    // loads of a stage hold up all that follows them: a CU takes about 16
-    // cycles for each.
-    auto step = [&](int s, s16x8 (&a)[TM], s16x8 (&b)[TN], s16x8 (&na)[TM], s16x8 (&nb)[TN]) {
-        ring_barrier<2 * kLoads>();
-        constexpr int kParts = TM >= 4 ? 4 : TM, kRows = TM / kParts;
+    // (B first: a lane then holds four consecutive columns of one row)
+    auto multiply = [&](int ih, int jh, int kk, const s16x8 (&a)[2][TI], const s16x8 (&b)[2][TJ]) {
 #pragma unroll
-        for (int c = 0; c < kParts; c++) {
+        for (int i = 0; i < TI; i++)
 #pragma unroll
-            for (int j = c; j < TN; j += kParts) nb[j] = read_b(s + 1, j);
+            for (int j = 0; j < TJ; j++)
+                acc[ih * TI + i][jh * TJ + j] = mfma16<DT>(b[kk][j], a[kk][i], acc[ih * TI + i][jh * TJ + j]);
+    };
+    // loads issued after the ones a phase waits for (the maps' among them)
+    constexpr int kWait3 = 2 * PA + 3 * PB + 2 * kMaps, kWait0 = 3 * PA + 2 * PB + 2 * kMaps;
+    // stage s of parity f, whose first B half is f: in rbf on entry, with A0 in ra0
+    auto stage = [&](int s, int f, s16x8 (&rbf)[2][TJ], s16x8 (&rbs)[2][TJ]) {
 #pragma unroll
-            for (int i = c * kRows; i < (c + 1) * kRows; i++) na[i] = read_a(s + 1, i);
-            // (B first: a lane then holds four consecutive columns of one row)
+        for (int p = 0; p < 4; p++) {
+            if (p == 0 || p == 1) phase_barrier<kWait0>();
+            if (p == 3) phase_barrier<kWait3>();
+            asm volatile("" : "+v"(a_at), "+v"(b_at));
+            ready(s + 2, p);
 #pragma unroll
-            for (int i = c * kRows; i < (c + 1) * kRows; i++)
+            for (int kk = 0; kk < 2; kk++) {
+                if (p == 0) read_b(f, 1 - f, kk, rbs);
+                if (p == 1) read_a(f, 1, kk, ra1);
+                if (p == 3) {
+                    read_a(1 - f, 0, kk, ra0);
+                    read_b(1 - f, 1 - f, kk, rbs);
+                }
+                if (p == 0) multiply(0, f, kk, ra0, rbf);
+                if (p == 1) multiply(0, 1 - f, kk, ra0, rbs);
+                if (p == 2) multiply(1, 1 - f, kk, ra1, rbs);
+                if (p == 3) multiply(1, f, kk, ra1, rbf);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < TN; j++) acc[i][j] = mfma16<DT>(b[j], a[i], acc[i][j]);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = c; i < kLoads; i += kParts) load_one(s + 4, i);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int i = kk; i < kLoads; i += 2) load(s + 2, f, p, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
     if (stages > 0) {
-        if (LAY == kGradWeights) {
-            // (the maps of the stages that the first loads go by)
-            for (int s = 0; s < 4; s++) fetch_maps(s);
+        if (kMaps) {
+            for (int s = 0; s < 4; s++) {
+                fetch_map(g.a, s, 0);
+                fetch_map(g.b, s, 1);
+            }
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            // load(s) fetches the maps of s + 3, load(0) of 3 again: the same values
         }
-        for (int s = 0; s < 4; s++) load(s);
-        ring_barrier<3 * kLoads>();
 #pragma unroll
-        for (int i = 0; i < TM; i++) fa[0][i] = read_a(0, i);
+        for (int s = 0; s < 2; s++)
 #pragma unroll
-        for (int j = 0; j < TN; j++) fb[0][j] = read_b(0, j);
+            for (int p = 0; p < 4; p++) {
+                ready(s, p);
+#pragma unroll
+                for (int i = 0; i < kLoads; i++) load(s, s, p, i);
+            }
+        phase_barrier<3 * PA + 3 * PB + 2 * kMaps>();
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            read_a(0, 0, kk, ra0);
+            read_b(0, 0, kk, rb0);
+        }
         for (int s = 0; s < stages; s += 2) {
-            step(s, fa[0], fb[0], fa[1], fb[1]);
+            stage(s, 0, rb0, rb1);
             if (s + 1 >= stages) break;
-            step(s + 1, fa[1], fb[1], fa[0], fb[0]);
+            stage(s + 1, 1, rb1, rb0);
         }
     }
-    // the epilogue writes where the ring's last loads go
-    ring_barrier<0>();
-    tile_epilogue<LAY, DT, TM, TN>(g, acc, reinterpret_cast<float *>(lds), srow + wm * (BM / WM), t.e,
-                                   n0 + wn * (BN / WN), wave, lane);
+    // the epilogue writes where the last loads go
+    phase_barrier<0>();
+    tile_epilogue<LAY, DT, BM, BN, 2>(g, acc, reinterpret_cast<float *>(lds), srow, t.e, n0, wm * (UM / WM),
+                                      wn * (UN / WN), wave, lane);
 }
 
 }  // namespace bm

@@ -19,6 +19,8 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
+constexpr int kBK = 64;             // contraction per stage
+
 // ---- elements -------------------------------------------------------------
 // DT: BITMOE_BF16 or BITMOE_F16
 template <int DT>
@@ -200,30 +202,27 @@ BM_DEV bool find_tile_dw(const GemmArgs &g, int mt, int nt, int bid, Tile *t) {
 }
 
 // ---- tiles in LDS ---------------------------------------------------------
-// An operand's stage is X rows of BK elements (contiguous along the
-// contraction: KC) or BK rows of X elements (KS), in 16-byte pieces.
+// An operand's stage is X rows of kBK elements (contiguous along the
+// contraction: KC) or kBK rows of X elements (KS), in 16-byte pieces.
 //  KC: piece c of row r at slot c ^ swz(r) of the row's pieces, so that the
 //      16-byte reads of consecutive rows, one piece each, run without bank
-//      conflicts (measured: 4.3 cycles for a wave's 1 KiB; (r >> 2) & 3 or
-//      padded rows of 64 + 16 bytes take 8.1, unswizzled rows of 128 16.2).
+//      conflicts (measured: 4.4 cycles for a wave's 1 KiB; rows padded by 16
+//      bytes take 8.2, rows neither padded nor swizzled 16.2).
 //  KS: pieces move in pairs of 32 bytes, pair c of row k at c ^ swz(k): a
 //      transposed read takes 32 bytes of each of 4 consecutive rows (8, 16, 24
 //      rows further for the wave's other lanes), and these fall on different
 //      banks too.
-template <int BK>
-BM_DEV int kc_swz(int r) {
-    return BK == 64 ? r & 7 : (r >> 1) & 3;
-}
+BM_DEV int kc_swz(int r) { return r & 7; }
 template <int X>
 BM_DEV int ks_swz(int k) {
     return X >= 128 ? (k & 3) | ((k >> 1) & 4) : (k & 3);
 }
 // piece p of the stage (in LDS order): its row and its piece in the row
-template <bool KC, int X, int BK>
+template <bool KC, int X>
 BM_DEV void piece_at(int p, int *row, int *col) {
     if (KC) {
-        *row = p / (BK / 8);
-        *col = p % (BK / 8) ^ kc_swz<BK>(*row);
+        *row = p / (kBK / 8);
+        *col = p % (kBK / 8) ^ kc_swz(*row);
     } else {
         *row = p / (X / 8);
         const int s = p % (X / 8);
@@ -232,12 +231,12 @@ BM_DEV void piece_at(int p, int *row, int *col) {
 }
 // the wave's matrix-core operand: 16 rows (KC) or columns (KS) from x0, 32 of
 // the contraction from kk; lane l holds row l % 16, contraction 8 (l / 16) + j
-template <bool KC, int X, int BK>
+template <bool KC, int X>
 BM_DEV s16x8 frag(const uint16_t *tile, int x0, int kk, int lane) {
     const int i = lane & 15, q = lane >> 4;
     if (KC) {
         const int row = x0 + i;
-        return *reinterpret_cast<const s16x8 *>(tile + row * BK + ((((kk >> 3) + q) ^ kc_swz<BK>(row)) << 3));
+        return *reinterpret_cast<const s16x8 *>(tile + row * kBK + ((((kk >> 3) + q) ^ kc_swz(row)) << 3));
     } else {
         // a transposing read: 16 lanes give 4 rows of 16 elements, four lanes
         // a row, and receive the 16 columns, 4 elements each
@@ -335,10 +334,13 @@ BM_DEV void set_rows(const GemmArgs &g, const Tile &t, int m0, int tid, int *sro
 // time) it takes 8 columns, so that 8 lanes (EW 64) write a whole 128-byte
 // line.  The pass over the wave's rows is a loop whose end moves the
 // accumulators down: one copy of the code, and no accumulator is indexed.
-// srow: the output row of each of the tile's rows, or -1.
-template <int LAY, int DT, int TM, int TN>
+// The wave's rows and columns come in HALVES equal runs, its own part of each
+// of the tile's halves of BM and BN: run h of rows at h * BM / 2 + m_at.  srow:
+// the output row of each of the tile's rows, or -1.
+template <int LAY, int DT, int BM, int BN, int HALVES, int TM, int TN>
 BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, const int *srow, int e, int n0,
-                          int wave, int lane) {
+                          int m_at, int n_at, int wave, int lane) {
+    constexpr int MR = 16 * TM / HALVES, NR = 16 * TN / HALVES;
     constexpr int QI = 2, EW = 16 * TN, LDW = EW + 4, LPR = EW / 8, RPI = 64 / LPR;
     static_assert(TM % QI == 0, "");
     float *sw = lds + wave * (16 * QI * LDW);
@@ -355,7 +357,8 @@ BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, c
             const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
             const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
             float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-            finish8<LAY, DT>(g, e, srow[16 * q + r], n0 + c, v);
+            const int m = 16 * q + r;
+            finish8<LAY, DT>(g, e, srow[m / MR * (BM / 2) + m_at + m % MR], n0 + c / NR * (BN / 2) + n_at + c % NR, v);
         }
 #pragma unroll
         for (int ii = 0; ii + QI < TM; ii++)
