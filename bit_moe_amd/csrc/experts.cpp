@@ -51,11 +51,13 @@ int check_ws(void *ws, size_t have, size_t need) {
     return BITMOE_OK;
 }
 
+bool span32(int rows, int64_t ld) { return ld < (1 << 30) && rows * ld < ((int64_t)1 << 31); }
+
 // Division by an invariant: with 2^(s-1) < d <= 2^s, m = floor(2^(31+s) / d) + 1
 // gives floor(x / d) = floor(x m / 2^(31+s)) for every x < 2^31 (the excess
 // m d - 2^(31+s) is at most d <= 2^s, so x times it stays below 2^(31+s)).
 GemmRows rows_arg(const bitmoe_rows *m) {
-    GemmRows r{m->data, m->map, m->ld, m->rows, 0, 0};
+    GemmRows r{m->data, m->map, m->ld, m->rows, 0, 0, span32(m->map ? m->rows : 256, m->ld)};
     if (m->map && m->div > 1) {
         uint32_t s = 0;
         while (((uint64_t)1 << s) < (uint64_t)m->div) s++;
@@ -64,7 +66,9 @@ GemmRows rows_arg(const bitmoe_rows *m) {
     }
     return r;
 }
-GemmRows weights_arg(const bitmoe_experts *w) { return GemmRows{w->data, nullptr, w->ld, w->N, 0, 0}; }
+GemmRows weights_arg(const bitmoe_experts *w) {
+    return GemmRows{w->data, nullptr, w->ld, w->N, 0, 0, span32(256, w->ld)};
+}
 
 // y = W x or dx = W^T dy over groups
 GemmArgs rows_product(const bitmoe_rows *a, const bitmoe_experts *w, const int32_t *offsets, int R,

@@ -14,6 +14,7 @@ struct GemmRows {
     int64_t ld;
     int32_t rows;
     uint32_t mul, shift;       // x / div = (x * mul >> 32) >> shift; mul 0: div 1
+    bool span32;               // the rows a tile may read together (all, by a map; else 256) span less than 4 GiB
 };
 
 // C[m][n] = sum_k A[m][k] B[n][k] over the groups of rows that `offsets`

@@ -141,8 +141,8 @@ int64_t tiles(const GemmArgs &g, int *mt, int *nt) {
     *nt = (g.N + BN - 1) / BN;
     // (rows: the tiles of all groups, at most)
     *mt = LAY == kGradWeights ? (g.M + BM - 1) / BM : g.R / BM + (g.E < g.R ? g.E : g.R);
-    const int64_t items = (LAY == kGradWeights ? g.E : 1) * (int64_t)*mt * *nt;
-    return (items + 7) / 8 * 8;
+    if (LAY == kGradWeights) return (int64_t)g.E * dw_eighth(*mt, *nt) * 8;
+    return ((int64_t)*mt * *nt + 7) / 8 * 8;
 }
 
 template <int LAY, int DT, int BM, int BN, int WM, int WN>

@@ -19,6 +19,8 @@
 // with its loads left out).
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_util.h"
 
 namespace bm {
@@ -29,11 +31,22 @@ __device__ const uint4 kZeroPiece = {0, 0, 0, 0};
 BM_DEV uint32_t lds_addr(const void *p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
+// a value that is the wave's, told to the compiler
+BM_DEV const uint16_t *wave_ptr(const uint16_t *p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const uint16_t *>((uint64_t)hi << 32 | lo);
+}
 // 16 (4) bytes per lane to LDS, lane l's at `lds` (one for the wave) + 16 l
 // (4 l).  In asm, because the compiler would wait for it before the next LDS
 // read, of whatever stage; phase_barrier() waits instead.
 BM_DEV void dma16(const void *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+// the same with a base of the wave's and 32-bit offsets (bytes) of the lanes':
+// no arithmetic per load
+BM_DEV void dma16_from(const void *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 BM_DEV void dma4(const void *src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
@@ -45,13 +58,13 @@ BM_DEV void phase_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// dynamic LDS of a tile: two stages; the output rows; for the weights'
+// dynamic LDS of a tile: two stages; the output rows; A's rows; for the weights'
 // gradient each wave's ring of row maps (64 of A's, 64 of B's, four stages).
 // The epilogue takes the stages' place.
 template <int LAY, int BM, int BN, int WM, int WN>
 struct TileLds {
     static constexpr int rows = 2 * (BM + BN) * kBK * 2;
-    static constexpr int maps = rows + BM * 4;
+    static constexpr int maps = rows + 2 * BM * 4;
     static constexpr int bytes = maps + (LAY == kGradWeights ? WM * WN * 4 * 128 * 4 : 0);
     static_assert(WM * WN * 32 * (BN / WN + 4) * 4 <= rows, "the epilogue's part");
     static_assert(bytes <= 160 * 1024, "");
@@ -121,34 +134,61 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     piece_at<BKC, UN>(tid, &br, &bc);
     constexpr int kRowA = AKC ? 8 * NW : 64 * NW * 8 / UM, kRowB = BKC ? 8 * NW : 64 * NW * 8 / UN;
     static_assert((kRowA % 16 == 0 || PA == 1) && (kRowB % 16 == 0 || PB == 1), "the swizzles' period");
-    // KC: each piece's address in the first stage, and whether it is there.
-    // Rows past the group, and columns past the matrix, read its last row
-    // (their results are not stored).
-    const uint16_t *ap[2][PA], *bp[2][PB];
-    bool ais[2][PA];
+    // Loads go by a base of the wave's that moves with the stage and offsets
+    // that stay, where the wave's rows are all there, the stage is whole and the
+    // operand spans less than 4 GiB; else, for that stage, by addresses made
+    // one by one, with the zero piece for what is not there.  Rows past the
+    // group, and columns past the matrix, read its last row (first columns):
+    // their results are not stored.
+    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::rows);
+    int *xrow = srow + BM;
+    const int whole = kend / kBK;                  // whole stages
+    uint32_t aoff[2][PA], boff[2][PB];
+    bool afast = g.a.span32, bfast = g.b.span32;
+    const uint16_t *abase = A, *bbase = B;         // of stage 0
+    int acol[2], bcol[2];                          // KS: the column within the matrix, per half
+    if (AKC) {
+        if (!g.a.map) abase += (int64_t)(t.r0 + m0) * g.a.ld;
+        bool there = true;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        if (AKC) {
+        for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int i = 0; i < PA; i++) {
-                const int row = row_of(g.a, min(t.r0 + m0 + h * UM + ar + i * kRowA, t.r1 - 1));
-                ais[h][i] = row >= 0;
-                ap[h][i] = A + (int64_t)max(row, 0) * g.a.ld + 8 * ac;
+                const int r = min(t.r0 + m0 + h * UM + ar + i * kRowA, t.r1 - 1), row = row_of(g.a, r);
+                there = there && row >= 0;
+                aoff[h][i] = (uint32_t)(max(row, 0) - (g.a.map ? 0 : t.r0 + m0)) * (uint32_t)g.a.ld * 2 + 16 * ac;
             }
+        afast = afast && __all(there);
+        if (tid < BM) xrow[tid] = row_of(g.a, min(t.r0 + m0 + tid, t.r1 - 1));
+    } else {
+        if (!g.a.map) abase += (int64_t)t.r0 * g.a.ld;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            acol[h] = m0 + h * UM + 8 * ac < g.M ? m0 + h * UM + 8 * ac : 0;
+#pragma unroll
+            for (int i = 0; i < PA; i++) aoff[h][i] = ((ar + i * kRowA) * (uint32_t)g.a.ld + acol[h]) * 2;
         }
-        if (BKC) {
+    }
+    if (BKC) {
+        bbase += (int64_t)n0 * g.b.ld;
+#pragma unroll
+        for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int i = 0; i < PB; i++)
-                bp[h][i] = B + (int64_t)min(n0 + h * UN + br + i * kRowB, g.N - 1) * g.b.ld + 8 * bc;
+                boff[h][i] = (uint32_t)min(h * UN + br + i * kRowB, g.N - 1 - n0) * (uint32_t)g.b.ld * 2 + 16 * bc;
+    } else {
+        if (kMaps && !g.b.map) bbase += (int64_t)t.r0 * g.b.ld;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            bcol[h] = n0 + h * UN + 8 * bc < g.N ? n0 + h * UN + 8 * bc : 0;
+#pragma unroll
+            for (int i = 0; i < PB; i++) boff[h][i] = ((br + i * kRowB) * (uint32_t)g.b.ld + bcol[h]) * 2;
         }
     }
-    // KS: the column within the matrix, per half
-    int acol[2], bcol[2];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        acol[h] = m0 + h * UM + 8 * ac < g.M ? m0 + h * UM + 8 * ac : 0;
-        bcol[h] = n0 + h * UN + 8 * bc < g.N ? n0 + h * UN + 8 * bc : 0;
-    }
+    A = wave_ptr(A);
+    B = wave_ptr(B);
+    abase = wave_ptr(abase);
+    bbase = wave_ptr(bbase);
     // The weights' gradient: the wave's own copy of the rows' maps, fetched two
     // stages before the loads that go by them; a stage's rows are resolved at
     // the operand's first unit and kept for its second.
@@ -168,60 +208,73 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         }
         return m < q.rows ? m : -1;
     };
-    const uint16_t *arow[PA], *brow[PB];
+    int arow[PA], brow[PB];                        // mapped rows of the stage being loaded
+    bool awhole = false, bwhole = false;           // they are all there
     const uint32_t lds0 = lds_addr(lds) + wave * 1024;
-    // load i of A's (B's) half h of stage s
-    auto load_a = [&](int s, int buf, int h, int i) {
-        const uint16_t *p;
-        if (AKC) {
-            p = s * kBK + 8 * ac < kend && ais[h][i] ? ap[h][i] + s * kBK : zero;
+    // load i of A's (B's) half h of stage s (fast: by the base, but for maps)
+    auto load_a = [&](auto fast, int s, int buf, int h, int i) {
+        const uint32_t to = lds0 + (buf * kStage + h * kUA) * 2 + i * (NW * 1024);
+        if (kMaps && g.a.map) {
+            if (awhole) dma16_from(A, (uint32_t)arow[i] * (uint32_t)g.a.ld * 2 + 2 * acol[h], to);
+            else dma16(arow[i] >= 0 ? A + (int64_t)arow[i] * g.a.ld + acol[h] : zero, to);
+        } else if (fast) {
+            dma16_from(abase + (int64_t)s * (AKC ? kBK : kBK * g.a.ld), aoff[h][i], to);
         } else {
-            p = arow[i] ? arow[i] + acol[h] : zero;
+            const int k = s * kBK + (AKC ? 8 * ac : ar + i * kRowA);
+            const int row = AKC ? xrow[h * UM + ar + i * kRowA] : t.r0 + k;
+            dma16(k < kend && row >= 0 ? A + (int64_t)row * g.a.ld + (AKC ? k : acol[h]) : zero, to);
         }
-        dma16(p, lds0 + (buf * kStage + h * kUA) * 2 + i * (NW * 1024));
     };
-    auto load_b = [&](int s, int buf, int h, int i) {
-        const uint16_t *p;
-        if (BKC) {
-            p = s * kBK + 8 * bc < kend ? bp[h][i] + s * kBK : zero;
-        } else if (kMaps) {
-            p = brow[i] ? brow[i] + bcol[h] : zero;
+    auto load_b = [&](auto fast, int s, int buf, int h, int i) {
+        const uint32_t to = lds0 + (buf * kStage + 2 * kUA + h * kUB) * 2 + i * (NW * 1024);
+        if (kMaps && g.b.map) {
+            if (bwhole) dma16_from(B, (uint32_t)brow[i] * (uint32_t)g.b.ld * 2 + 2 * bcol[h], to);
+            else dma16(brow[i] >= 0 ? B + (int64_t)brow[i] * g.b.ld + bcol[h] : zero, to);
+        } else if (fast) {
+            dma16_from(bbase + (int64_t)s * (BKC ? kBK : kBK * g.b.ld), boff[h][i], to);
         } else {
-            const int k = s * kBK + br + i * kRowB;
-            p = k < kend ? B + (int64_t)k * g.b.ld + bcol[h] : zero;
+            const int k = s * kBK + (BKC ? 8 * bc : br + i * kRowB);
+            const int row = BKC ? min(n0 + h * UN + br + i * kRowB, g.N - 1) : kMaps ? t.r0 + k : k;
+            dma16(k < kend ? B + (int64_t)row * g.b.ld + (BKC ? k : bcol[h]) : zero, to);
         }
-        dma16(p, lds0 + (buf * kStage + 2 * kUA + h * kUB) * 2 + i * (NW * 1024));
     };
     // what the unit of phase p of stage s needs before its loads
     auto ready = [&](int s, int p) {
         if (!kMaps || p > 1) return;
         if (p == 0) {
+            if (g.a.map) {
+                bool there = true;
 #pragma unroll
-            for (int i = 0; i < PA; i++) {
-                const int r = map_row(g.a, 0, s, ar + i * kRowA);
-                arow[i] = r >= 0 ? A + (int64_t)r * g.a.ld : nullptr;
+                for (int i = 0; i < PA; i++) {
+                    arow[i] = map_row(g.a, 0, s, ar + i * kRowA);
+                    there = there && arow[i] >= 0;
+                }
+                awhole = afast && __all(there);
             }
             fetch_map(g.a, s + 2, 0);
         } else {
+            if (g.b.map) {
+                bool there = true;
 #pragma unroll
-            for (int i = 0; i < PB; i++) {
-                const int r = map_row(g.b, 1, s, br + i * kRowB);
-                brow[i] = r >= 0 ? B + (int64_t)r * g.b.ld : nullptr;
+                for (int i = 0; i < PB; i++) {
+                    brow[i] = map_row(g.b, 1, s, br + i * kRowB);
+                    there = there && brow[i] >= 0;
+                }
+                bwhole = bfast && __all(there);
             }
             fetch_map(g.b, s + 2, 1);
         }
     };
     // the loads of phase p for stage s, of parity f: its place in LDS, and B's
     // half that comes first
-    auto load = [&](int s, int f, int p, int i) {
+    auto load = [&](auto fast, int s, int f, int p, int i) {
         if (p == 0 || p == 3) {
-            if (i < PA) load_a(s, f, p == 3, i);
+            if (i < PA) load_a(fast, s, f, p == 3, i);
         } else if (i < PB) {
-            load_b(s, f, p == 1 ? f : 1 - f, i);
+            load_b(fast, s, f, p == 1 ? f : 1 - f, i);
         }
     };
     constexpr int kLoads = PA > PB ? PA : PB;
-    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::rows);
     set_rows<LAY, BM>(g, t, m0, tid, srow);
 
     f32x4 acc[2 * TI][2 * TJ];
@@ -252,7 +305,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     // loads issued after the ones a phase waits for (the maps' among them)
     constexpr int kWait3 = 2 * PA + 3 * PB + 2 * kMaps, kWait0 = 3 * PA + 2 * PB + 2 * kMaps;
     // stage s of parity f, whose first B half is f: in rbf on entry, with A0 in ra0
-    auto stage = [&](int s, int f, s16x8 (&rbf)[2][TJ], s16x8 (&rbs)[2][TJ]) {
+    auto stage = [&](auto fast, int s, int f, s16x8 (&rbf)[2][TJ], s16x8 (&rbs)[2][TJ]) {
 #pragma unroll
         for (int p = 0; p < 4; p++) {
             if (p == 0 || p == 1) phase_barrier<kWait0>();
@@ -273,12 +326,13 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
                 if (p == 3) multiply(1, f, kk, ra1, rbf);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = kk; i < kLoads; i += 2) load(s + 2, f, p, i);
+                for (int i = kk; i < kLoads; i += 2) load(fast, s + 2, f, p, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
     if (stages > 0) {
+        if (AKC) __syncthreads();          // xrow
         if (kMaps) {
             for (int s = 0; s < 4; s++) {
                 fetch_map(g.a, s, 0);
@@ -292,7 +346,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             for (int p = 0; p < 4; p++) {
                 ready(s, p);
 #pragma unroll
-                for (int i = 0; i < kLoads; i++) load(s, s, p, i);
+                for (int i = 0; i < kLoads; i++) load(std::false_type{}, s, s, p, i);
             }
         phase_barrier<3 * PA + 3 * PB + 2 * kMaps>();
 #pragma unroll
@@ -300,10 +354,16 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             read_a(0, 0, kk, ra0);
             read_b(0, 0, kk, rb0);
         }
-        for (int s = 0; s < stages; s += 2) {
-            stage(s, 0, rb0, rb1);
+        int s = 0;
+        if ((afast || (kMaps && g.a.map)) && (bfast || (kMaps && g.b.map)))
+            for (; s + 3 < whole; s += 2) {
+                stage(std::true_type{}, s, 0, rb0, rb1);
+                stage(std::true_type{}, s + 1, 1, rb1, rb0);
+            }
+        for (; s < stages; s += 2) {
+            stage(std::false_type{}, s, 0, rb0, rb1);
             if (s + 1 >= stages) break;
-            stage(s + 1, 1, rb1, rb0);
+            stage(std::false_type{}, s + 1, 1, rb1, rb0);
         }
     }
     // the epilogue writes where the last loads go

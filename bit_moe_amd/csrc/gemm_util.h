@@ -115,6 +115,21 @@ BM_DEV void store8(void *p, int64_t i, int n, bool f32, const float *v) {
     }
 }
 
+// eight values, or one
+template <int DT>
+BM_DEV void load_row(const void *p, int64_t i, bool f32, float (&v)[8]) { load8<DT>(p, i, 8, f32, v); }
+template <int DT>
+BM_DEV void store_row(void *p, int64_t i, bool f32, const float (&v)[8]) { store8<DT>(p, i, 8, f32, v); }
+template <int DT>
+BM_DEV void load_row(const void *p, int64_t i, bool f32, float (&v)[1]) {
+    v[0] = f32 ? static_cast<const float *>(p)[i] : elem_f32<DT>(static_cast<const uint16_t *>(p)[i]);
+}
+template <int DT>
+BM_DEV void store_row(void *p, int64_t i, bool f32, const float (&v)[1]) {
+    if (f32) static_cast<float *>(p)[i] = v[0];
+    else static_cast<uint16_t *>(p)[i] = (uint16_t)elem_pair<DT>(v[0], 0.f);
+}
+
 // ---- rows and groups ------------------------------------------------------
 // m / div for 0 <= m < 2^31 (the multiplier and shift of rows_arg)
 BM_DEV int divided(const GemmRows &q, int m) { return q.mul ? (int)(__umulhi((uint32_t)m, q.mul) >> q.shift) : m; }
@@ -185,19 +200,19 @@ BM_DEV bool find_tile(const GemmArgs &g, int nt, int bid, Tile *t) {
     t->n = __builtin_amdgcn_readfirstlane(rem / mb);
     return true;
 }
-// the same for the weights' gradient, whose tiles are fixed: (expert, 8 row
-// tiles by all column tiles at a time)
+// The same for the weights' gradient, whose tiles are fixed but not their work
+// (a group's rows): each XCD takes an eighth of every expert's tiles.
+__host__ __device__ inline int dw_eighth(int mt, int nt) { return (mt * nt + 7) / 8; }
 BM_DEV bool find_tile_dw(const GemmArgs &g, int mt, int nt, int bid, Tile *t) {
-    const int64_t items = (int64_t)g.E * mt * nt, per_xcd = (items + 7) / 8;
-    const int64_t item = (int64_t)(bid & 7) * per_xcd + (bid >> 3);
-    if ((bid >> 3) >= per_xcd || item >= items) return false;
-    t->e = (int)(item / ((int64_t)mt * nt));
-    const int idx = (int)(item - (int64_t)t->e * mt * nt);
+    const int per = dw_eighth(mt, nt);
+    t->e = (bid >> 3) / per;
+    const int idx = (bid & 7) * per + (bid >> 3) - t->e * per;
+    if (t->e >= g.E || idx >= mt * nt) return false;
     const int blk = idx / (8 * nt), mb = min(8, mt - 8 * blk), rem = idx - blk * 8 * nt;
     t->m = 8 * blk + rem % mb;
     t->n = rem / mb;
-    t->r0 = group_start(g, t->e);
-    t->r1 = max(group_start(g, t->e + 1), t->r0);
+    t->r0 = __builtin_amdgcn_readfirstlane(group_start(g, t->e));
+    t->r1 = max(__builtin_amdgcn_readfirstlane(group_start(g, t->e + 1)), t->r0);
     return true;
 }
 
@@ -264,6 +279,20 @@ BM_DEV float act_fwd(float z, int act) {
     }
 }
 
+template <int W>
+BM_DEV void act_row(float (&v)[W], int act) {
+#define BM_ACT(A)                                                   \
+    case A:                                                         \
+        _Pragma("unroll") for (int j = 0; j < W; j++) v[j] = act_fwd(v[j], A); \
+        break;
+    switch (act) {
+        BM_ACT(BITMOE_ACT_RELU)
+        BM_ACT(BITMOE_ACT_GELU)
+        BM_ACT(BITMOE_ACT_GELU_TANH)
+        BM_ACT(BITMOE_ACT_SILU)
+    }
+#undef BM_ACT
+}
 // d act / dz
 BM_DEV float act_slope(float z, int act) {
     switch (act) {
@@ -283,41 +312,35 @@ BM_DEV float act_slope(float z, int act) {
     }
 }
 
-// eight outputs of a row: n.. of row `row` of the output
-template <int LAY, int DT>
-BM_DEV void finish8(const GemmArgs &g, int e, int row, int n, float *v) {
-    const int left = g.N - n;
-    if (left <= 0 || row < 0) return;
+// Eight (W = 8) outputs of a row, or the one at the edge (W = 1): n.. of row
+// `row` of the output.  res: the residual's, loaded before.
+template <int LAY, int DT, int W>
+BM_DEV void finish(const GemmArgs &g, int e, int row, int n, float (&v)[W], const float (&res)[W]) {
     int64_t at = (int64_t)row * g.c.ld + n;
     if constexpr (LAY == kGradWeights) {
         at += (int64_t)e * g.c_stride;
         if (g.accumulate) {
-            float o[8];
-            load8<DT>(g.c.p, at, left, g.c_f32, o);
+            float o[W];
+            load_row<DT>(g.c.p, at, g.c_f32, o);
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] += o[j];
+            for (int j = 0; j < W; j++) v[j] += o[j];
         }
     }
     if constexpr (LAY == kForward) {
         if (g.bias) {
-            float o[8];
-            load8<DT>(g.bias, n, left, false, o);
+            float o[W];
+            load_row<DT>(g.bias, n, false, o);
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] += o[j];
+            for (int j = 0; j < W; j++) v[j] += o[j];
         }
-        if (g.pre) store8<DT>(g.pre, (int64_t)row * g.ld_pre + n, left, false, v);
-        if (g.act != BITMOE_ACT_NONE) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = act_fwd(v[j], g.act);
-        }
+        if (g.pre) store_row<DT>(g.pre, (int64_t)row * g.ld_pre + n, false, v);
+        if (g.act != BITMOE_ACT_NONE) act_row(v, g.act);
         if (g.res) {
-            float o[8];
-            load8<DT>(g.res, (int64_t)row * g.ld_res + n, left, g.res_f32, o);
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] += o[j];
+            for (int j = 0; j < W; j++) v[j] += res[j];
         }
     }
-    store8<DT>(const_cast<void *>(g.c.p), at, left, g.c_f32, v);
+    store_row<DT>(const_cast<void *>(g.c.p), at, g.c_f32, v);
 }
 
 // the output row of each of a tile's rows, or -1
@@ -331,9 +354,9 @@ BM_DEV void set_rows(const GemmArgs &g, const Tile &t, int m0, int tid, int *sro
 
 // The waves' accumulators to memory.  A lane holds 4 columns of one row of
 // each 16 x 16 product; through LDS (a wave's own part of `lds`, 32 rows at a
-// time) it takes 8 columns, so that 8 lanes (EW 64) write a whole 128-byte
-// line.  The pass over the wave's rows is a loop whose end moves the
-// accumulators down: one copy of the code, and no accumulator is indexed.
+// time) it takes 8 columns, so that 8 lanes (EW 64) write 128 bytes.  The
+// passes over the wave's rows are loops whose ends move the registers down:
+// one copy of the code (unrolled it was 60 KB), and no register is indexed.
 // The wave's rows and columns come in HALVES equal runs, its own part of each
 // of the tile's halves of BM and BN: run h of rows at h * BM / 2 + m_at.  srow:
 // the output row of each of the tile's rows, or -1.
@@ -341,24 +364,47 @@ template <int LAY, int DT, int BM, int BN, int HALVES, int TM, int TN>
 BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, const int *srow, int e, int n0,
                           int m_at, int n_at, int wave, int lane) {
     constexpr int MR = 16 * TM / HALVES, NR = 16 * TN / HALVES;
-    constexpr int QI = 2, EW = 16 * TN, LDW = EW + 4, LPR = EW / 8, RPI = 64 / LPR;
+    constexpr int QI = 2, EW = 16 * TN, LDW = EW + 4, LPR = EW / 8, RPI = 64 / LPR, IT = 16 * QI / RPI;
     static_assert(TM % QI == 0, "");
     float *sw = lds + wave * (16 * QI * LDW);
+    const int r0 = lane / LPR, c = (lane % LPR) * 8, n = n0 + c / NR * (BN / 2) + n_at + c % NR, left = g.N - n;
+    auto out_row = [&](int m) { return srow[m / MR * (BM / 2) + m_at + m % MR]; };
 #pragma unroll 1
     for (int q = 0; q < TM; q += QI) {
+        float res[IT][8];
+        if (LAY == kForward && g.res && left >= 8) {
+#pragma unroll
+            for (int it = 0; it < IT; it++) {
+                const int row = out_row(16 * q + it * RPI + r0);
+                load_row<DT>(g.res, (int64_t)max(row, 0) * g.ld_res + n, g.res_f32, res[it]);
+            }
+        }
 #pragma unroll
         for (int ii = 0; ii < QI; ii++)
 #pragma unroll
             for (int j = 0; j < TN; j++)
                 *reinterpret_cast<f32x4 *>(sw + (16 * ii + (lane & 15)) * LDW + 16 * j + 4 * (lane >> 4)) = acc[ii][j];
+#pragma unroll 1
+        for (int it = 0; it < IT; it++) {
+            const int r = it * RPI + r0, row = out_row(16 * q + r);
+            if (row >= 0 && left >= 8) {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
+                float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                finish<LAY, DT>(g, e, row, n, v, res[0]);
+            } else if (row >= 0) {
+                for (int j = 0; j < left; j++) {
+                    float v[1] = {sw[r * LDW + c + j]}, one[1] = {0.f};
+                    if (LAY == kForward && g.res) load_row<DT>(g.res, (int64_t)row * g.ld_res + n + j, g.res_f32, one);
+                    finish<LAY, DT>(g, e, row, n + j, v, one);
+                }
+            }
+            if (LAY == kForward) {
 #pragma unroll
-        for (int it = 0; it < 16 * QI / RPI; it++) {
-            const int r = it * RPI + lane / LPR, c = (lane % LPR) * 8;
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
-            float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-            const int m = 16 * q + r;
-            finish8<LAY, DT>(g, e, srow[m / MR * (BM / 2) + m_at + m % MR], n0 + c / NR * (BN / 2) + n_at + c % NR, v);
+                for (int i = 0; i + 1 < IT; i++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) res[i][j] = res[i + 1][j];
+            }
         }
 #pragma unroll
         for (int ii = 0; ii + QI < TM; ii++)
