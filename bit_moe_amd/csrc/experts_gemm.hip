@@ -5,11 +5,14 @@
 // k_gemm: rows of any alignment.  A workgroup of 4 waves makes a 128 x 128
 // tile (64 x 64 a wave); a stage of 64 of the contraction is loaded into
 // registers while the one before it is multiplied out of LDS.
+#include <algorithm>
+
 #include "gemm_tile.h"
 
 namespace {
 
 using namespace bm;
+using bm_host::cu_count;
 
 
 // 8 elements of an operand's stage: row `row` of the rows it runs along
@@ -31,15 +34,15 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     constexpr int NT = 64 * WM * WN, PA = BM * kBK / 8 / NT, PB = BN * kBK / 8 / NT;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr bool AKC = LAY != kGradWeights, BKC = LAY == kForward;
-    // the stage, and after it the epilogue's rows (32 of BN / WN + 4 floats a wave)
-    __shared__ __attribute__((aligned(16))) uint16_t lds[WM * WN * 32 * (BN / WN + 4) * 2];
-    static_assert(sizeof(lds) >= (BM + BN) * kBK * 2, "");
+    // the stage, and after it the epilogue's part
+    __shared__ __attribute__((aligned(16))) uint16_t lds[(BM + BN) * kBK];
+    static_assert(sizeof(lds) >= WM * WN * epilogue_floats<TN>() * 4, "");
     __shared__ int srow[BM];
     uint16_t *sa = lds, *sb = lds + BM * kBK;
     Tile t;
-    if (LAY == kGradWeights ? !find_tile_dw(g, mtiles, ntiles, blockIdx.x, &t)
-                            : !find_tile<BM>(g, ntiles, blockIdx.x, &t))
-        return;
+    Tiles<LAY, BM> list;
+    list.init(g, mtiles, ntiles, blockIdx.x, gridDim.x);
+    if (!list.next(g, &t) || t.m < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int m0 = t.m * BM, n0 = t.n * BN;
@@ -149,12 +152,13 @@ template <int LAY, int DT, int BM, int BN, int WM, int WN>
 int launch_tile(const GemmArgs &g, hipStream_t s) {
     int mt, nt;
     const int64_t grid = tiles<LAY, BM, BN>(g, &mt, &nt);
-    if (grid * 64 * WM * WN >= (int64_t)1 << 32) return BITMOE_EUNSUPPORTED;
     constexpr int lds = TileLds<LAY, BM, BN, WM, WN>::bytes;
+    // as many workgroups as fit the GPU together, each for several tiles
+    const int64_t most = (int64_t)cu_count() * (160 * 1024 / lds);
     // (LDS above 64 KiB must be opted into per kernel and device)
     (void)hipFuncSetAttribute(reinterpret_cast<const void *>(k_gemm_tile<LAY, DT, BM, BN, WM, WN>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    k_gemm_tile<LAY, DT, BM, BN, WM, WN><<<(int)grid, 64 * WM * WN, lds, s>>>(g, mt, nt);
+    k_gemm_tile<LAY, DT, BM, BN, WM, WN><<<(int)std::min(grid, std::max<int64_t>(most / 8 * 8, 8)), 64 * WM * WN, lds, s>>>(g, mt, nt);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }

@@ -58,15 +58,16 @@ BM_DEV void phase_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// dynamic LDS of a tile: two stages; the output rows; A's rows; for the weights'
-// gradient each wave's ring of row maps (64 of A's, 64 of B's, four stages).
-// The epilogue takes the stages' place.
+// Dynamic LDS of a workgroup: two stages; the output rows of this tile and the
+// next; A's rows; for the weights' gradient a ring of row maps (64 of A's, 64 of
+// B's, four stages); the epilogue's part, which is its own, so that the next
+// tile's first stages can be on their way during it.
 template <int LAY, int BM, int BN, int WM, int WN>
 struct TileLds {
     static constexpr int rows = 2 * (BM + BN) * kBK * 2;
-    static constexpr int maps = rows + 2 * BM * 4;
-    static constexpr int bytes = maps + (LAY == kGradWeights ? WM * WN * 4 * 128 * 4 : 0);
-    static_assert(WM * WN * 32 * (BN / WN + 4) * 4 <= rows, "the epilogue's part");
+    static constexpr int maps = rows + 3 * BM * 4;
+    static constexpr int out = maps + (LAY == kGradWeights ? 4 * 128 * 4 : 0);
+    static constexpr int bytes = out + WM * WN * epilogue_floats<BN / WN / 16>() * 4;
     static_assert(bytes <= 160 * 1024, "");
 };
 
@@ -113,17 +114,10 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW, "");
     extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
     Tile t;
-    if (LAY == kGradWeights ? !find_tile_dw(g, mtiles, ntiles, blockIdx.x, &t)
-                            : !find_tile<BM>(g, ntiles, blockIdx.x, &t))
-        return;
+    Tiles<LAY, BM> list;
+    list.init(g, mtiles, ntiles, blockIdx.x, gridDim.x);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int m0 = t.m * BM, n0 = t.n * BN;
-    const int kend = LAY == kGradWeights ? t.r1 - t.r0 : g.K;
-    const int stages = (kend + kBK - 1) / kBK;
-    const uint16_t *A = static_cast<const uint16_t *>(g.a.p);
-    const uint16_t *B = static_cast<const uint16_t *>(g.b.p);
-    if (LAY != kGradWeights) B += (int64_t)t.e * g.b_stride;
     const uint16_t *zero = reinterpret_cast<const uint16_t *>(&kZeroPiece);
 
     // Piece i of this thread in a unit, in LDS order: tid + 64 NW i.  Its
@@ -134,65 +128,78 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     piece_at<BKC, UN>(tid, &br, &bc);
     constexpr int kRowA = AKC ? 8 * NW : 64 * NW * 8 / UM, kRowB = BKC ? 8 * NW : 64 * NW * 8 / UN;
     static_assert((kRowA % 16 == 0 || PA == 1) && (kRowB % 16 == 0 || PB == 1), "the swizzles' period");
-    // Loads go by a base of the wave's that moves with the stage and offsets
-    // that stay, where the wave's rows are all there, the stage is whole and the
-    // operand spans less than 4 GiB; else, for that stage, by addresses made
-    // one by one, with the zero piece for what is not there.  Rows past the
-    // group, and columns past the matrix, read its last row (first columns):
-    // their results are not stored.
+    // What the loads of a tile go by.  By a base of the wave's that moves with
+    // the stage and offsets that stay, where the wave's rows are all there, the
+    // stage is whole and the operand spans less than 4 GiB; else, for that
+    // stage, by addresses made one by one, with the zero piece for what is not
+    // there.  Rows past the group, and columns past the matrix, read its last
+    // row (first columns): their results are not stored.
     int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::rows);
-    int *xrow = srow + BM;
-    const int whole = kend / kBK;                  // whole stages
-    uint32_t aoff[2][PA], boff[2][PB];
-    bool afast = g.a.span32, bfast = g.b.span32;
-    const uint16_t *abase = A, *bbase = B;         // of stage 0
-    int acol[2], bcol[2];                          // KS: the column within the matrix, per half
-    if (AKC) {
-        if (!g.a.map) abase += (int64_t)(t.r0 + m0) * g.a.ld;
-        bool there = true;
+    int *xrow = srow + 2 * BM;
+    int m0, n0, kend, stages, whole;               // whole: whole stages
+    const uint16_t *A, *B, *abase, *bbase;         // the matrices; what stage 0 goes by
+    uint32_t aoff[AKC ? 2 * PA : PA + 2], boff[BKC ? 2 * PB : PB + 2];   // bytes: KC by half and piece;
+    bool afast, bfast;                                                   // KS the rows', then the halves' columns
+    auto enter = [&](int par) {
+        m0 = t.m * BM;
+        n0 = t.n * BN;
+        kend = LAY == kGradWeights ? t.r1 - t.r0 : g.K;
+        stages = (kend + kBK - 1) / kBK;
+        whole = kend / kBK;
+        afast = g.a.span32;
+        bfast = g.b.span32;
+        A = static_cast<const uint16_t *>(g.a.p);
+        B = static_cast<const uint16_t *>(g.b.p);
+        if (LAY != kGradWeights) B += (int64_t)t.e * g.b_stride;
+        abase = A;
+        bbase = B;
+        if (AKC) {
+            if (!g.a.map) abase += (int64_t)(t.r0 + m0) * g.a.ld;
+            bool there = true;
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+            for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int i = 0; i < PA; i++) {
-                const int r = min(t.r0 + m0 + h * UM + ar + i * kRowA, t.r1 - 1), row = row_of(g.a, r);
-                there = there && row >= 0;
-                aoff[h][i] = (uint32_t)(max(row, 0) - (g.a.map ? 0 : t.r0 + m0)) * (uint32_t)g.a.ld * 2 + 16 * ac;
-            }
-        afast = afast && __all(there);
-        if (tid < BM) xrow[tid] = row_of(g.a, min(t.r0 + m0 + tid, t.r1 - 1));
-    } else {
-        if (!g.a.map) abase += (int64_t)t.r0 * g.a.ld;
+                for (int i = 0; i < PA; i++) {
+                    const int r = min(t.r0 + m0 + h * UM + ar + i * kRowA, t.r1 - 1), row = row_of(g.a, r);
+                    there = there && row >= 0;
+                    aoff[h * PA + i] = (uint32_t)(max(row, 0) - (g.a.map ? 0 : t.r0 + m0)) * (uint32_t)g.a.ld * 2 + 16 * ac;
+                }
+            afast = afast && __all(there);
+            if (tid < BM) xrow[tid] = row_of(g.a, min(t.r0 + m0 + tid, t.r1 - 1));
+        } else {
+            if (!g.a.map) abase += (int64_t)t.r0 * g.a.ld;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            acol[h] = m0 + h * UM + 8 * ac < g.M ? m0 + h * UM + 8 * ac : 0;
+            for (int i = 0; i < PA; i++) aoff[i] = (ar + i * kRowA) * (uint32_t)g.a.ld * 2;
 #pragma unroll
-            for (int i = 0; i < PA; i++) aoff[h][i] = ((ar + i * kRowA) * (uint32_t)g.a.ld + acol[h]) * 2;
+            for (int h = 0; h < 2; h++)
+                aoff[PA + h] = m0 + h * UM + 8 * ac < g.M ? (m0 + h * UM + 8 * ac) * 2 : 0;
         }
-    }
-    if (BKC) {
-        bbase += (int64_t)n0 * g.b.ld;
+        if (BKC) {
+            bbase += (int64_t)n0 * g.b.ld;
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+            for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int i = 0; i < PB; i++)
-                boff[h][i] = (uint32_t)min(h * UN + br + i * kRowB, g.N - 1 - n0) * (uint32_t)g.b.ld * 2 + 16 * bc;
-    } else {
-        if (kMaps && !g.b.map) bbase += (int64_t)t.r0 * g.b.ld;
+                for (int i = 0; i < PB; i++)
+                    boff[h * PB + i] = (uint32_t)min(h * UN + br + i * kRowB, g.N - 1 - n0) * (uint32_t)g.b.ld * 2 + 16 * bc;
+        } else {
+            if (kMaps && !g.b.map) bbase += (int64_t)t.r0 * g.b.ld;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            bcol[h] = n0 + h * UN + 8 * bc < g.N ? n0 + h * UN + 8 * bc : 0;
+            for (int i = 0; i < PB; i++) boff[i] = (br + i * kRowB) * (uint32_t)g.b.ld * 2;
 #pragma unroll
-            for (int i = 0; i < PB; i++) boff[h][i] = ((br + i * kRowB) * (uint32_t)g.b.ld + bcol[h]) * 2;
+            for (int h = 0; h < 2; h++)
+                boff[PB + h] = n0 + h * UN + 8 * bc < g.N ? (n0 + h * UN + 8 * bc) * 2 : 0;
         }
-    }
-    A = wave_ptr(A);
-    B = wave_ptr(B);
-    abase = wave_ptr(abase);
-    bbase = wave_ptr(bbase);
-    // The weights' gradient: the wave's own copy of the rows' maps, fetched two
-    // stages before the loads that go by them; a stage's rows are resolved at
-    // the operand's first unit and kept for its second.
-    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::maps) + wave * 512;
+        A = wave_ptr(A);
+        B = wave_ptr(B);
+        abase = wave_ptr(abase);
+        bbase = wave_ptr(bbase);
+        set_rows<LAY, BM>(g, t, m0, tid, srow + par * BM);
+    };
+    // The weights' gradient: the rows' maps, fetched two stages before the loads
+    // that go by them; a stage's rows are resolved at the operand's first unit
+    // and kept for its second.  Every wave fetches them all, to the same place
+    // (the same values), and so waits only for its own loads.
+    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::maps);
     const uint32_t maps_at = lds_addr(maps);
     auto fetch_map = [&](const GemmRows &q, int s, int b) {
         const int k = min(s * kBK + lane, kend - 1);
@@ -208,62 +215,53 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         }
         return m < q.rows ? m : -1;
     };
-    int arow[PA], brow[PB];                        // mapped rows of the stage being loaded
-    bool awhole = false, bwhole = false;           // they are all there
+    bool awhole = false, bwhole = false;           // mapped rows of the stage being loaded: all there
     const uint32_t lds0 = lds_addr(lds) + wave * 1024;
     // load i of A's (B's) half h of stage s (fast: by the base, but for maps)
     auto load_a = [&](auto fast, int s, int buf, int h, int i) {
         const uint32_t to = lds0 + (buf * kStage + h * kUA) * 2 + i * (NW * 1024);
-        if (kMaps && g.a.map) {
-            if (awhole) dma16_from(A, (uint32_t)arow[i] * (uint32_t)g.a.ld * 2 + 2 * acol[h], to);
-            else dma16(arow[i] >= 0 ? A + (int64_t)arow[i] * g.a.ld + acol[h] : zero, to);
-        } else if (fast) {
-            dma16_from(abase + (int64_t)s * (AKC ? kBK : kBK * g.a.ld), aoff[h][i], to);
+        if (AKC) {
+            if (fast) return dma16_from(abase + (int64_t)s * kBK, aoff[h * PA + i], to);
+            const int k = s * kBK + 8 * ac, row = xrow[h * UM + ar + i * kRowA];
+            dma16(k < kend && row >= 0 ? A + (int64_t)row * g.a.ld + k : zero, to);
         } else {
-            const int k = s * kBK + (AKC ? 8 * ac : ar + i * kRowA);
-            const int row = AKC ? xrow[h * UM + ar + i * kRowA] : t.r0 + k;
-            dma16(k < kend && row >= 0 ? A + (int64_t)row * g.a.ld + (AKC ? k : acol[h]) : zero, to);
+            const bool mapped = g.a.map != nullptr;
+            if (mapped ? awhole : fast)
+                return dma16_from(mapped ? A : abase + (int64_t)s * kBK * g.a.ld, aoff[i] + aoff[PA + h], to);
+            const int row = map_row(g.a, 0, s, ar + i * kRowA);
+            dma16(row >= 0 ? A + (int64_t)row * g.a.ld + aoff[PA + h] / 2 : zero, to);
         }
     };
     auto load_b = [&](auto fast, int s, int buf, int h, int i) {
         const uint32_t to = lds0 + (buf * kStage + 2 * kUA + h * kUB) * 2 + i * (NW * 1024);
-        if (kMaps && g.b.map) {
-            if (bwhole) dma16_from(B, (uint32_t)brow[i] * (uint32_t)g.b.ld * 2 + 2 * bcol[h], to);
-            else dma16(brow[i] >= 0 ? B + (int64_t)brow[i] * g.b.ld + bcol[h] : zero, to);
-        } else if (fast) {
-            dma16_from(bbase + (int64_t)s * (BKC ? kBK : kBK * g.b.ld), boff[h][i], to);
+        if (BKC) {
+            if (fast) return dma16_from(bbase + (int64_t)s * kBK, boff[h * PB + i], to);
+            const int k = s * kBK + 8 * bc;
+            dma16(k < kend ? B + (int64_t)min(n0 + h * UN + br + i * kRowB, g.N - 1) * g.b.ld + k : zero, to);
         } else {
-            const int k = s * kBK + (BKC ? 8 * bc : br + i * kRowB);
-            const int row = BKC ? min(n0 + h * UN + br + i * kRowB, g.N - 1) : kMaps ? t.r0 + k : k;
-            dma16(k < kend ? B + (int64_t)row * g.b.ld + (BKC ? k : bcol[h]) : zero, to);
+            const bool mapped = kMaps && g.b.map != nullptr;
+            if (mapped ? bwhole : fast)
+                return dma16_from(mapped ? B : bbase + (int64_t)s * kBK * g.b.ld, boff[i] + boff[PB + h], to);
+            const int k = s * kBK + br + i * kRowB;
+            const int row = kMaps ? map_row(g.b, 1, s, br + i * kRowB) : k < kend ? k : -1;
+            dma16(row >= 0 ? B + (int64_t)row * g.b.ld + boff[PB + h] / 2 : zero, to);
         }
     };
     // what the unit of phase p of stage s needs before its loads
     auto ready = [&](int s, int p) {
         if (!kMaps || p > 1) return;
-        if (p == 0) {
-            if (g.a.map) {
-                bool there = true;
+        const GemmRows &q = p == 0 ? g.a : g.b;
+        if (q.map) {
+            bool there = true;
 #pragma unroll
-                for (int i = 0; i < PA; i++) {
-                    arow[i] = map_row(g.a, 0, s, ar + i * kRowA);
-                    there = there && arow[i] >= 0;
-                }
-                awhole = afast && __all(there);
+            for (int i = 0; i < (p == 0 ? PA : PB); i++) {
+                const int row = map_row(q, p, s, p == 0 ? ar + i * kRowA : br + i * kRowB);
+                there = there && row >= 0;
+                (p == 0 ? aoff[i] : boff[i]) = (uint32_t)row * (uint32_t)q.ld * 2;
             }
-            fetch_map(g.a, s + 2, 0);
-        } else {
-            if (g.b.map) {
-                bool there = true;
-#pragma unroll
-                for (int i = 0; i < PB; i++) {
-                    brow[i] = map_row(g.b, 1, s, br + i * kRowB);
-                    there = there && brow[i] >= 0;
-                }
-                bwhole = bfast && __all(there);
-            }
-            fetch_map(g.b, s + 2, 1);
+            (p == 0 ? awhole : bwhole) = (p == 0 ? afast : bfast) && __all(there);
         }
+        fetch_map(q, s + 2, p);
     };
     // the loads of phase p for stage s, of parity f: its place in LDS, and B's
     // half that comes first
@@ -275,13 +273,8 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         }
     };
     constexpr int kLoads = PA > PB ? PA : PB;
-    set_rows<LAY, BM>(g, t, m0, tid, srow);
 
     f32x4 acc[2 * TI][2 * TJ];
-#pragma unroll
-    for (int i = 0; i < 2 * TI; i++)
-#pragma unroll
-        for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     s16x8 ra0[2][TI], ra1[2][TI], rb0[2][TJ], rb1[2][TJ];       // [half of the stage's contraction]
     static_assert((TI & (TI - 1)) == 0 && (TJ & (TJ - 1)) == 0 && kUA % 512 == 0 && kUB % 512 == 0, "frag_at");
     uint32_t a_at = frag_place<AKC, UM>(lds_addr(lds), wm * (UM / WM), lane);
@@ -331,8 +324,9 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             }
         }
     };
-    if (stages > 0) {
-        if (AKC) __syncthreads();          // xrow
+    // the loads of a tile's first two stages
+    auto begin = [&]() {
+        if (stages == 0) return;
         if (kMaps) {
             for (int s = 0; s < 4; s++) {
                 fetch_map(g.a, s, 0);
@@ -340,36 +334,67 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             }
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
+        auto both = [&](auto fast) {
 #pragma unroll
-        for (int s = 0; s < 2; s++)
+            for (int s = 0; s < 2; s++)
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                ready(s, p);
+                for (int p = 0; p < 4; p++) {
+                    ready(s, p);
 #pragma unroll
-                for (int i = 0; i < kLoads; i++) load(std::false_type{}, s, s, p, i);
+                    for (int i = 0; i < kLoads; i++) load(fast, s, s, p, i);
+                }
+        };
+        if (afast && bfast && whole >= 2) both(std::true_type{});
+        else both(std::false_type{});
+    };
+    // a tile that is there
+    auto next = [&]() {
+        do
+            if (!list.next(g, &t)) return false;
+        while (LAY == kGradWeights && t.m < 0);
+        return true;
+    };
+    if (!next()) return;
+    enter(0);
+    __syncthreads();           // xrow
+    begin();
+    for (int par = 0;; par ^= 1) {
+#pragma unroll
+        for (int i = 0; i < 2 * TI; i++)
+#pragma unroll
+            for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (stages > 0) {
+            phase_barrier<3 * PA + 3 * PB + 2 * kMaps>();
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                read_a(0, 0, kk, ra0);
+                read_b(0, 0, kk, rb0);
             }
-        phase_barrier<3 * PA + 3 * PB + 2 * kMaps>();
-#pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            read_a(0, 0, kk, ra0);
-            read_b(0, 0, kk, rb0);
-        }
-        int s = 0;
-        if ((afast || (kMaps && g.a.map)) && (bfast || (kMaps && g.b.map)))
-            for (; s + 3 < whole; s += 2) {
-                stage(std::true_type{}, s, 0, rb0, rb1);
-                stage(std::true_type{}, s + 1, 1, rb1, rb0);
+            int s = 0;
+            if ((afast || (kMaps && g.a.map)) && (bfast || (kMaps && g.b.map)))
+                for (; s + 3 < whole; s += 2) {
+                    stage(std::true_type{}, s, 0, rb0, rb1);
+                    stage(std::true_type{}, s + 1, 1, rb1, rb0);
+                }
+            for (; s < stages; s += 2) {
+                stage(std::false_type{}, s, 0, rb0, rb1);
+                if (s + 1 >= stages) break;
+                stage(std::false_type{}, s + 1, 1, rb1, rb0);
             }
-        for (; s < stages; s += 2) {
-            stage(std::false_type{}, s, 0, rb0, rb1);
-            if (s + 1 >= stages) break;
-            stage(std::false_type{}, s + 1, 1, rb1, rb0);
         }
+        // every wave is done with the stages, and the loads past the last
+        // stage have arrived: the next tile's may begin
+        phase_barrier<0>();
+        const int e = t.e, n = n0;
+        const bool more = next();
+        if (more) enter(par ^ 1);
+        __syncthreads();       // xrow; srow, where no stage was
+        if (more) begin();
+        tile_epilogue<LAY, DT, BM, BN, 2>(
+            g, acc, reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::out),
+            srow + par * BM, e, n, wm * (UM / WM), wn * (UN / WN), wave, lane);
+        if (!more) return;
     }
-    // the epilogue writes where the last loads go
-    phase_barrier<0>();
-    tile_epilogue<LAY, DT, BM, BN, 2>(g, acc, reinterpret_cast<float *>(lds), srow, t.e, n0, wm * (UM / WM),
-                                      wn * (UN / WN), wave, lane);
 }
 
 }  // namespace bm

@@ -154,67 +154,87 @@ struct Tile {
     int m, n;           // tile indexes
 };
 
-// A workgroup's tile among the (expert, row tile, column tile) of the groups.
-// Every wave finds it by itself: each lane counts the row tiles of a run of
-// experts, a scan over the lanes gives their places.  Workgroups go round
-// the 8 XCDs in turn, so consecutive tiles are given to workgroups of one
-// XCD, whose L2 then serves the operands they share; within an expert, 8 row
-// tiles by all column tiles at a time.
-template <int BM>
-BM_DEV bool find_tile(const GemmArgs &g, int nt, int bid, Tile *t) {
-    const int lane = lane_id(), per = (g.E + 63) / 64;
-    int mine = 0;
-    for (int i = 0; i < per; i++) {
-        const int e = lane * per + i;
-        if (e < g.E) mine += (max(group_start(g, e + 1) - group_start(g, e), 0) + BM - 1) / BM;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(incl, o, kWave);
-        if (lane >= o) incl += v;
-    }
-    const int total = __shfl(incl, 63, kWave);
-    const int64_t items = (int64_t)total * nt;
-    const int64_t per_xcd = (items + 7) / 8;
-    const int64_t item = (int64_t)(bid & 7) * per_xcd + (bid >> 3);
-    if ((bid >> 3) >= per_xcd || item >= items) return false;
-    const int mt = (int)(item / nt);         // as a place among the row tiles
-    const uint64_t has = __ballot(mt < incl);
-    const int src = __builtin_ctzll(has);    // the first lane whose run reaches past it
-    int base = __shfl(incl - mine, src, kWave), e = src * per;
-    int cnt, r0, r1;
-    for (;; e++) {
-        r0 = group_start(g, e);
-        r1 = group_start(g, e + 1);
-        cnt = (max(r1 - r0, 0) + BM - 1) / BM;
-        if (mt < base + cnt || e >= g.E - 1) break;
-        base += cnt;
-    }
-    const int idx = (int)(item - (int64_t)base * nt);
-    const int blk = idx / (8 * nt), mb = min(8, cnt - 8 * blk), rem = idx - blk * 8 * nt;
-    t->e = __builtin_amdgcn_readfirstlane(e);
-    t->r0 = __builtin_amdgcn_readfirstlane(r0);
-    t->r1 = __builtin_amdgcn_readfirstlane(r1);
-    t->m = __builtin_amdgcn_readfirstlane(8 * blk + rem % mb);
-    t->n = __builtin_amdgcn_readfirstlane(rem / mb);
-    return true;
-}
-// The same for the weights' gradient, whose tiles are fixed but not their work
-// (a group's rows): each XCD takes an eighth of every expert's tiles.
+// The tiles of a workgroup.  Workgroups go round the 8 XCDs in turn; each XCD
+// has its own list of tiles, whose neighbours share operands through its L2,
+// and its workgroups take them in order.
+//  Rows (forward, rows' gradient): the (expert, row tile, column tile) of all
+//   groups, one after another, 8 row tiles by all column tiles at a time, are
+//   cut into 8 runs.  Every wave counts the groups' row tiles by itself: each
+//   lane those of a run of experts, and a scan over the lanes places them.
+//  Weights' gradient: the tiles are fixed, their work (a group's rows) is not:
+//   each XCD takes an eighth of every expert's tiles.
 __host__ __device__ inline int dw_eighth(int mt, int nt) { return (mt * nt + 7) / 8; }
-BM_DEV bool find_tile_dw(const GemmArgs &g, int mt, int nt, int bid, Tile *t) {
-    const int per = dw_eighth(mt, nt);
-    t->e = (bid >> 3) / per;
-    const int idx = (bid & 7) * per + (bid >> 3) - t->e * per;
-    if (t->e >= g.E || idx >= mt * nt) return false;
-    const int blk = idx / (8 * nt), mb = min(8, mt - 8 * blk), rem = idx - blk * 8 * nt;
-    t->m = 8 * blk + rem % mb;
-    t->n = rem / mb;
-    t->r0 = __builtin_amdgcn_readfirstlane(group_start(g, t->e));
-    t->r1 = max(__builtin_amdgcn_readfirstlane(group_start(g, t->e + 1)), t->r0);
-    return true;
-}
+
+template <int LAY, int BM>
+struct Tiles {
+    int xcd, slot, step;       // the next tile's place in the XCD's list
+    int per, mine, incl;       // rows: experts a lane counts, their row tiles, with all lanes' before
+    int mt, nt;                // dw: row tiles; column tiles
+    int64_t items, per_xcd;
+
+    BM_DEV void init(const GemmArgs &g, int mtiles, int ntiles, int bid, int grid) {
+        xcd = bid & 7;
+        slot = bid >> 3;
+        step = grid >> 3;
+        mt = mtiles;
+        nt = ntiles;
+        if (LAY == kGradWeights) return;
+        const int lane = lane_id();
+        per = (g.E + 63) / 64;
+        mine = 0;
+        for (int i = 0; i < per; i++) {
+            const int e = lane * per + i;
+            if (e < g.E) mine += (max(group_start(g, e + 1) - group_start(g, e), 0) + BM - 1) / BM;
+        }
+        incl = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o, kWave);
+            if (lane >= o) incl += v;
+        }
+        items = (int64_t)__builtin_amdgcn_readlane(incl, 63) * nt;
+        per_xcd = (items + 7) / 8;
+    }
+    BM_DEV bool next(const GemmArgs &g, Tile *t) {
+        const int at = slot;
+        slot += step;
+        int idx, cnt;
+        if (LAY == kGradWeights) {
+            const int n8 = dw_eighth(mt, nt);
+            t->e = at / n8;
+            idx = xcd * n8 + at - t->e * n8;
+            cnt = mt;
+            if (t->e >= g.E) return false;
+            if (idx >= mt * nt) {                  // the eighths are not whole: none here
+                t->m = -1;
+                return true;
+            }
+            t->r0 = __builtin_amdgcn_readfirstlane(group_start(g, t->e));
+            t->r1 = max(__builtin_amdgcn_readfirstlane(group_start(g, t->e + 1)), t->r0);
+        } else {
+            const int64_t item = xcd * per_xcd + at;
+            if (at >= per_xcd || item >= items) return false;
+            const int place = (int)(item / nt);                          // among the row tiles
+            const int src = __builtin_ctzll(__ballot(place < incl));     // the lane whose run holds it
+            int base = __builtin_amdgcn_readlane(incl - mine, src), e = src * per, r0, r1;
+            for (;; e++) {
+                r0 = group_start(g, e);
+                r1 = group_start(g, e + 1);
+                cnt = (max(r1 - r0, 0) + BM - 1) / BM;
+                if (place < base + cnt || e >= g.E - 1) break;
+                base += cnt;
+            }
+            idx = (int)(item - (int64_t)base * nt);
+            t->e = __builtin_amdgcn_readfirstlane(e);
+            t->r0 = __builtin_amdgcn_readfirstlane(r0);
+            t->r1 = __builtin_amdgcn_readfirstlane(r1);
+        }
+        const int blk = idx / (8 * nt), mb = min(8, cnt - 8 * blk), rem = idx - blk * 8 * nt;
+        t->m = __builtin_amdgcn_readfirstlane(8 * blk + rem % mb);
+        t->n = __builtin_amdgcn_readfirstlane(rem / mb);
+        return true;
+    }
+};
 
 // ---- tiles in LDS ---------------------------------------------------------
 // An operand's stage is X rows of kBK elements (contiguous along the
@@ -313,9 +333,10 @@ BM_DEV float act_slope(float z, int act) {
 }
 
 // Eight (W = 8) outputs of a row, or the one at the edge (W = 1): n.. of row
-// `row` of the output.  res: the residual's, loaded before.
+// `row` of the output, with the bias's and the residual's values.
 template <int LAY, int DT, int W>
-BM_DEV void finish(const GemmArgs &g, int e, int row, int n, float (&v)[W], const float (&res)[W]) {
+BM_DEV void finish(const GemmArgs &g, int e, int row, int n, float (&v)[W], const float (&bias)[W],
+                   const float (&res)[W]) {
     int64_t at = (int64_t)row * g.c.ld + n;
     if constexpr (LAY == kGradWeights) {
         at += (int64_t)e * g.c_stride;
@@ -328,10 +349,8 @@ BM_DEV void finish(const GemmArgs &g, int e, int row, int n, float (&v)[W], cons
     }
     if constexpr (LAY == kForward) {
         if (g.bias) {
-            float o[W];
-            load_row<DT>(g.bias, n, false, o);
 #pragma unroll
-            for (int j = 0; j < W; j++) v[j] += o[j];
+            for (int j = 0; j < W; j++) v[j] += bias[j];
         }
         if (g.pre) store_row<DT>(g.pre, (int64_t)row * g.ld_pre + n, false, v);
         if (g.act != BITMOE_ACT_NONE) act_row(v, g.act);
@@ -353,63 +372,136 @@ BM_DEV void set_rows(const GemmArgs &g, const Tile &t, int m0, int tid, int *sro
 }
 
 // The waves' accumulators to memory.  A lane holds 4 columns of one row of
-// each 16 x 16 product; through LDS (a wave's own part of `lds`, 32 rows at a
-// time) it takes 8 columns, so that 8 lanes (EW 64) write 128 bytes.  The
-// passes over the wave's rows are loops whose ends move the registers down:
-// one copy of the code (unrolled it was 60 KB), and no register is indexed.
+// each 16 x 16 product; through LDS (a wave's own part of `lds`) it takes 8
+// columns, 16 rows by half the wave's columns at a time.
 // The wave's rows and columns come in HALVES equal runs, its own part of each
 // of the tile's halves of BM and BN: run h of rows at h * BM / 2 + m_at.  srow:
 // the output row of each of the tile's rows, or -1.
+// Where there is nothing to add and the tile ends inside the matrix, the code
+// is unrolled.  Else the pass over the rows is a loop whose end moves the
+// accumulators down, one copy of that much longer code and no register indexed;
+// the moves alone take 4 us a tile of 256 x 256, so the short form is worth its
+// code.
+// Lanes hand values to each other through LDS between these points: the wave's
+// LDS operations run in order, and the point keeps the compiler from letting
+// some lanes run ahead (it may otherwise give lanes without a row a path of
+// their own through the passes, whose writes then overtake the others' reads).
+BM_DEV void wave_together() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int TN>
+constexpr int epilogue_floats() { return 16 * (8 * TN + 4); }       // a wave's part
+
 template <int LAY, int DT, int BM, int BN, int HALVES, int TM, int TN>
 BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, const int *srow, int e, int n0,
                           int m_at, int n_at, int wave, int lane) {
-    constexpr int MR = 16 * TM / HALVES, NR = 16 * TN / HALVES;
-    constexpr int QI = 2, EW = 16 * TN, LDW = EW + 4, LPR = EW / 8, RPI = 64 / LPR, IT = 16 * QI / RPI;
-    static_assert(TM % QI == 0, "");
-    float *sw = lds + wave * (16 * QI * LDW);
-    const int r0 = lane / LPR, c = (lane % LPR) * 8, n = n0 + c / NR * (BN / 2) + n_at + c % NR, left = g.N - n;
+    constexpr int MR = 16 * TM / HALVES, TH = TN / 2, CW = 16 * TH;      // columns at a time
+    constexpr int LDW = CW + 4, LPR = CW / 8, RPI = 64 / LPR, IT = 16 / RPI;
+    static_assert(TN % 2 == 0 && (HALVES == 2 || HALVES == 1), "");
+    float *sw = lds + wave * epilogue_floats<TN>();
+    const int r0 = lane / LPR, c = (lane % LPR) * 8;
+    const int nn[2] = {n0 + n_at + c, n0 + n_at + c + (HALVES == 2 ? BN / 2 : CW)};
     auto out_row = [&](int m) { return srow[m / MR * (BM / 2) + m_at + m % MR]; };
+    const bool has_res = LAY == kForward && g.res;
+    const bool plain = LAY == kForward ? !g.bias && !g.pre && !g.res && g.act == BITMOE_ACT_NONE : !g.accumulate;
+    if (plain && n0 + BN <= g.N) {
+        char *out = static_cast<char *>(const_cast<void *>(g.c.p));
+        const int es = g.c_f32 ? 4 : 2;
+        if (LAY == kGradWeights) out += (int64_t)e * g.c_stride * es;
+#pragma unroll
+        for (int q = 0; q < TM; q++) {
+            int rows[IT];
+#pragma unroll
+            for (int it = 0; it < IT; it++) rows[it] = out_row(16 * q + it * RPI + r0);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+#pragma unroll
+                for (int j = 0; j < TH; j++)
+                    *reinterpret_cast<f32x4 *>(sw + (lane & 15) * LDW + 16 * j + 4 * (lane >> 4)) = acc[q][h * TH + j];
+                wave_together();
+#pragma unroll
+                for (int it = 0; it < IT; it++) {
+                    const int r = it * RPI + r0;
+                    const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
+                    const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
+                    if (rows[it] < 0) continue;
+                    char *p = out + ((int64_t)rows[it] * g.c.ld + nn[h]) * es;
+                    if (g.c_f32) {
+                        reinterpret_cast<F128 *>(p)[0] = F128{{a[0], a[1], a[2], a[3]}};
+                        reinterpret_cast<F128 *>(p)[1] = F128{{b[0], b[1], b[2], b[3]}};
+                    } else {
+                        *reinterpret_cast<U128 *>(p) = U128{{elem_pair<DT>(a[0], a[1]), elem_pair<DT>(a[2], a[3]),
+                                                             elem_pair<DT>(b[0], b[1]), elem_pair<DT>(b[2], b[3])}};
+                    }
+                }
+                wave_together();
+            }
+        }
+        return;
+    }
+    auto residual = [&](int q, int h, int it, float (&r)[8]) {
+        const int row = out_row(16 * q + it * RPI + r0);
+        if (has_res && row >= 0 && nn[h] + 8 <= g.N)
+            load_row<DT>(g.res, (int64_t)row * g.ld_res + nn[h], g.res_f32, r);
+    };
+    // (the residual one pass ahead of its use)
+    float res[2][IT][8], ahead[2][IT][8], bias[2][8];
+    if (LAY == kForward) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (g.bias && nn[h] + 8 <= g.N) load_row<DT>(g.bias, nn[h], false, bias[h]);
+#pragma unroll
+            for (int it = 0; it < IT; it++) residual(0, h, it, res[h][it]);
+        }
+    }
 #pragma unroll 1
-    for (int q = 0; q < TM; q += QI) {
-        float res[IT][8];
-        if (LAY == kForward && g.res && left >= 8) {
+    for (int q = 0; q < TM; q++) {
+        if (LAY == kForward && q + 1 < TM) {
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int it = 0; it < IT; it++) residual(q + 1, h, it, ahead[h][it]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+            for (int j = 0; j < TH; j++)
+                *reinterpret_cast<f32x4 *>(sw + (lane & 15) * LDW + 16 * j + 4 * (lane >> 4)) = acc[0][h * TH + j];
+            wave_together();
 #pragma unroll
             for (int it = 0; it < IT; it++) {
-                const int row = out_row(16 * q + it * RPI + r0);
-                load_row<DT>(g.res, (int64_t)max(row, 0) * g.ld_res + n, g.res_f32, res[it]);
-            }
-        }
-#pragma unroll
-        for (int ii = 0; ii < QI; ii++)
-#pragma unroll
-            for (int j = 0; j < TN; j++)
-                *reinterpret_cast<f32x4 *>(sw + (16 * ii + (lane & 15)) * LDW + 16 * j + 4 * (lane >> 4)) = acc[ii][j];
+                const int r = it * RPI + r0, row = out_row(16 * q + r), left = g.N - nn[h];
+                if (row >= 0 && left >= 8) {
+                    const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
+                    const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
+                    float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                    finish<LAY, DT>(g, e, row, nn[h], v, bias[h], res[h][it]);
+                } else if (row >= 0) {
 #pragma unroll 1
-        for (int it = 0; it < IT; it++) {
-            const int r = it * RPI + r0, row = out_row(16 * q + r);
-            if (row >= 0 && left >= 8) {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
-                const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
-                float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-                finish<LAY, DT>(g, e, row, n, v, res[0]);
-            } else if (row >= 0) {
-                for (int j = 0; j < left; j++) {
-                    float v[1] = {sw[r * LDW + c + j]}, one[1] = {0.f};
-                    if (LAY == kForward && g.res) load_row<DT>(g.res, (int64_t)row * g.ld_res + n + j, g.res_f32, one);
-                    finish<LAY, DT>(g, e, row, n + j, v, one);
+                    for (int j = 0; j < left; j++) {
+                        float v[1] = {sw[r * LDW + c + j]}, one[1] = {0.f}, bi[1] = {0.f};
+                        if (LAY == kForward && g.bias) load_row<DT>(g.bias, nn[h] + j, false, bi);
+                        if (has_res) load_row<DT>(g.res, (int64_t)row * g.ld_res + nn[h] + j, g.res_f32, one);
+                        finish<LAY, DT>(g, e, row, nn[h] + j, v, bi, one);
+                    }
                 }
             }
-            if (LAY == kForward) {
+            wave_together();
+        }
+        if (LAY == kForward) {
 #pragma unroll
-                for (int i = 0; i + 1 < IT; i++)
+            for (int h = 0; h < 2; h++)
 #pragma unroll
-                    for (int j = 0; j < 8; j++) res[i][j] = res[i + 1][j];
-            }
+                for (int it = 0; it < IT; it++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) res[h][it][j] = ahead[h][it][j];
         }
 #pragma unroll
-        for (int ii = 0; ii + QI < TM; ii++)
+        for (int i = 0; i + 1 < TM; i++)
 #pragma unroll
-            for (int j = 0; j < TN; j++) acc[ii][j] = acc[ii + QI][j];
+            for (int j = 0; j < TN; j++) acc[i][j] = acc[i + 1][j];
     }
 }
 
