@@ -41,11 +41,31 @@ struct GemmArgs {
     void *pre;
     int64_t ld_res, ld_pre;
     bool res_f32;              // (bias and pre are of the operands' type)
+    // a split contraction: `splits` parts of kper (kGradWeights: of the group's
+    // rows in equal whole stages), each to its own C, c_split elements further
+    int32_t splits, kper;
+    int64_t c_split;
 };
 
-// workspace of a product: a rule on the host-known sizes (E, R, M, N, K)
+// How a product runs: which kernel, its tiles, into how many parts the
+// contraction is split.  A rule on the sizes the host knows.
+enum GemmKind { kAny, kTile256, kTile128x256, kTile128, kTile64x128 };
+struct GemmPlan {
+    int kind;
+    int mt, nt;         // row tiles (of all groups, at most; kGradWeights: of an expert), column tiles
+    int splits, kper;
+    int64_t grid;       // workgroups that would take one tile each
+    size_t ws;
+};
+// every row begins on a 16-byte address and has whole 8-element pieces
+bool gemm_whole(int layout, const GemmArgs &g);
+GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole);
+// workspace of a product of these sizes, whatever its addresses
 size_t gemm_ws_bytes(int layout, const GemmArgs &g);
 int launch_gemm(int layout, int dtype, const GemmArgs &g, void *ws, hipStream_t s);
+int launch_experts_fwd(int dtype, const GemmArgs &g, const GemmPlan &p, hipStream_t s);
+int launch_experts_dx(int dtype, const GemmArgs &g, const GemmPlan &p, hipStream_t s);
+int launch_experts_dw(int dtype, const GemmArgs &g, const GemmPlan &p, hipStream_t s);
 
 // dz = dy act'(pre) (dz may be NULL) and, with db, its column sums by slices
 // of rows (partial [slices][N])

@@ -115,7 +115,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
     Tile t;
     Tiles<LAY, BM> list;
-    list.init(g, mtiles, ntiles, blockIdx.x, gridDim.x);
+    list.init(g, mtiles, ntiles * g.splits, blockIdx.x, gridDim.x);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const uint16_t *zero = reinterpret_cast<const uint16_t *>(&kZeroPiece);
@@ -136,16 +136,19 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     // row (first columns): their results are not stored.
     int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::rows);
     int *xrow = srow + 2 * BM;
-    int m0, n0, kend, stages, whole;               // whole: whole stages
+    int m0, n0, kbeg, kend, split, stages, whole;  // whole: whole stages
     const uint16_t *A, *B, *abase, *bbase;         // the matrices; what stage 0 goes by
     uint32_t aoff[AKC ? 2 * PA : PA + 2], boff[BKC ? 2 * PB : PB + 2];   // bytes: KC by half and piece;
     bool afast, bfast;                                                   // KS the rows', then the halves' columns
     auto enter = [&](int par) {
+        const Span k = span_of<LAY>(g, &t, ntiles);
         m0 = t.m * BM;
         n0 = t.n * BN;
-        kend = LAY == kGradWeights ? t.r1 - t.r0 : g.K;
-        stages = (kend + kBK - 1) / kBK;
-        whole = kend / kBK;
+        kbeg = k.beg;
+        kend = k.end;
+        split = k.split;
+        stages = (kend - kbeg + kBK - 1) / kBK;
+        whole = (kend - kbeg) / kBK;
         afast = g.a.span32;
         bfast = g.b.span32;
         A = static_cast<const uint16_t *>(g.a.p);
@@ -154,6 +157,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         abase = A;
         bbase = B;
         if (AKC) {
+            abase += kbeg;
             if (!g.a.map) abase += (int64_t)(t.r0 + m0) * g.a.ld;
             bool there = true;
 #pragma unroll
@@ -175,14 +179,15 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
                 aoff[PA + h] = m0 + h * UM + 8 * ac < g.M ? (m0 + h * UM + 8 * ac) * 2 : 0;
         }
         if (BKC) {
-            bbase += (int64_t)n0 * g.b.ld;
+            bbase += (int64_t)n0 * g.b.ld + kbeg;
 #pragma unroll
             for (int h = 0; h < 2; h++)
 #pragma unroll
                 for (int i = 0; i < PB; i++)
                     boff[h * PB + i] = (uint32_t)min(h * UN + br + i * kRowB, g.N - 1 - n0) * (uint32_t)g.b.ld * 2 + 16 * bc;
         } else {
-            if (kMaps && !g.b.map) bbase += (int64_t)t.r0 * g.b.ld;
+            if (!kMaps) bbase += (int64_t)kbeg * g.b.ld;
+            else if (!g.b.map) bbase += (int64_t)t.r0 * g.b.ld;
 #pragma unroll
             for (int i = 0; i < PB; i++) boff[i] = (br + i * kRowB) * (uint32_t)g.b.ld * 2;
 #pragma unroll
@@ -222,7 +227,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         const uint32_t to = lds0 + (buf * kStage + h * kUA) * 2 + i * (NW * 1024);
         if (AKC) {
             if (fast) return dma16_from(abase + (int64_t)s * kBK, aoff[h * PA + i], to);
-            const int k = s * kBK + 8 * ac, row = xrow[h * UM + ar + i * kRowA];
+            const int k = kbeg + s * kBK + 8 * ac, row = xrow[h * UM + ar + i * kRowA];
             dma16(k < kend && row >= 0 ? A + (int64_t)row * g.a.ld + k : zero, to);
         } else {
             const bool mapped = g.a.map != nullptr;
@@ -236,13 +241,13 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         const uint32_t to = lds0 + (buf * kStage + 2 * kUA + h * kUB) * 2 + i * (NW * 1024);
         if (BKC) {
             if (fast) return dma16_from(bbase + (int64_t)s * kBK, boff[h * PB + i], to);
-            const int k = s * kBK + 8 * bc;
+            const int k = kbeg + s * kBK + 8 * bc;
             dma16(k < kend ? B + (int64_t)min(n0 + h * UN + br + i * kRowB, g.N - 1) * g.b.ld + k : zero, to);
         } else {
             const bool mapped = kMaps && g.b.map != nullptr;
             if (mapped ? bwhole : fast)
                 return dma16_from(mapped ? B : bbase + (int64_t)s * kBK * g.b.ld, boff[i] + boff[PB + h], to);
-            const int k = s * kBK + br + i * kRowB;
+            const int k = kbeg + s * kBK + br + i * kRowB;
             const int row = kMaps ? map_row(g.b, 1, s, br + i * kRowB) : k < kend ? k : -1;
             dma16(row >= 0 ? B + (int64_t)row * g.b.ld + boff[PB + h] / 2 : zero, to);
         }
@@ -385,14 +390,14 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         // every wave is done with the stages, and the loads past the last
         // stage have arrived: the next tile's may begin
         phase_barrier<0>();
-        const int e = t.e, n = n0;
+        const int e = t.e, n = n0, part = split;
         const bool more = next();
         if (more) enter(par ^ 1);
         __syncthreads();       // xrow; srow, where no stage was
         if (more) begin();
         tile_epilogue<LAY, DT, BM, BN, 2>(
             g, acc, reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::out),
-            srow + par * BM, e, n, wm * (UM / WM), wn * (UN / WN), wave, lane);
+            srow + par * BM, e, part, n, wm * (UM / WM), wn * (UN / WN), wave, lane);
         if (!more) return;
     }
 }

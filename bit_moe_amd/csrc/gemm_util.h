@@ -236,6 +236,32 @@ struct Tiles {
     }
 };
 
+// The part of the contraction that a tile takes: [beg, end) of it, and which
+// part it is (the column tiles of the list are those of the parts, one part
+// after another).  Weights' gradient: the group's rows become the part's.
+struct Span {
+    int beg, end, split;
+};
+template <int LAY>
+BM_DEV Span span_of(const GemmArgs &g, Tile *t, int nt) {
+    Span k{0, LAY == kGradWeights ? t->r1 - t->r0 : g.K, 0};
+    if (g.splits > 1) {
+        k.split = t->n / nt;
+        t->n -= k.split * nt;
+        if (LAY == kGradWeights) {
+            const int per = ((k.end + kBK - 1) / kBK + g.splits - 1) / g.splits * kBK;
+            const int r0 = min(t->r0 + k.split * per, t->r1);
+            t->r1 = min(r0 + per, t->r1);
+            t->r0 = r0;
+            k.end = t->r1 - r0;
+        } else {
+            k.beg = min(k.split * g.kper, g.K);
+            k.end = min(k.beg + g.kper, g.K);
+        }
+    }
+    return k;
+}
+
 // ---- tiles in LDS ---------------------------------------------------------
 // An operand's stage is X rows of kBK elements (contiguous along the
 // contraction: KC) or kBK rows of X elements (KS), in 16-byte pieces.
@@ -333,11 +359,12 @@ BM_DEV float act_slope(float z, int act) {
 }
 
 // Eight (W = 8) outputs of a row, or the one at the edge (W = 1): n.. of row
-// `row` of the output, with the bias's and the residual's values.
+// `row` of the output, with the bias's and the residual's values;
+// part: where a part of a split begins.
 template <int LAY, int DT, int W>
-BM_DEV void finish(const GemmArgs &g, int e, int row, int n, float (&v)[W], const float (&bias)[W],
+BM_DEV void finish(const GemmArgs &g, int e, int64_t part, int row, int n, float (&v)[W], const float (&bias)[W],
                    const float (&res)[W]) {
-    int64_t at = (int64_t)row * g.c.ld + n;
+    int64_t at = part + (int64_t)row * g.c.ld + n;
     if constexpr (LAY == kGradWeights) {
         at += (int64_t)e * g.c_stride;
         if (g.accumulate) {
@@ -395,8 +422,8 @@ template <int TN>
 constexpr int epilogue_floats() { return 16 * (8 * TN + 4); }       // a wave's part
 
 template <int LAY, int DT, int BM, int BN, int HALVES, int TM, int TN>
-BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, const int *srow, int e, int n0,
-                          int m_at, int n_at, int wave, int lane) {
+BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, const int *srow, int e, int split,
+                          int n0, int m_at, int n_at, int wave, int lane) {
     constexpr int MR = 16 * TM / HALVES, TH = TN / 2, CW = 16 * TH;      // columns at a time
     constexpr int LDW = CW + 4, LPR = CW / 8, RPI = 64 / LPR, IT = 16 / RPI;
     static_assert(TN % 2 == 0 && (HALVES == 2 || HALVES == 1), "");
@@ -405,11 +432,13 @@ BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, c
     const int nn[2] = {n0 + n_at + c, n0 + n_at + c + (HALVES == 2 ? BN / 2 : CW)};
     auto out_row = [&](int m) { return srow[m / MR * (BM / 2) + m_at + m % MR]; };
     const bool has_res = LAY == kForward && g.res;
+
     const bool plain = LAY == kForward ? !g.bias && !g.pre && !g.res && g.act == BITMOE_ACT_NONE : !g.accumulate;
     if (plain && n0 + BN <= g.N) {
         char *out = static_cast<char *>(const_cast<void *>(g.c.p));
         const int es = g.c_f32 ? 4 : 2;
         if (LAY == kGradWeights) out += (int64_t)e * g.c_stride * es;
+        out += split * g.c_split * es;
 #pragma unroll
         for (int q = 0; q < TM; q++) {
             int rows[IT];
@@ -477,14 +506,14 @@ BM_DEV void tile_epilogue(const GemmArgs &g, f32x4 (&acc)[TM][TN], float *lds, c
                     const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
                     const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
                     float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-                    finish<LAY, DT>(g, e, row, nn[h], v, bias[h], res[h][it]);
+                    finish<LAY, DT>(g, e, split * g.c_split, row, nn[h], v, bias[h], res[h][it]);
                 } else if (row >= 0) {
 #pragma unroll 1
                     for (int j = 0; j < left; j++) {
                         float v[1] = {sw[r * LDW + c + j]}, one[1] = {0.f}, bi[1] = {0.f};
                         if (LAY == kForward && g.bias) load_row<DT>(g.bias, nn[h] + j, false, bi);
                         if (has_res) load_row<DT>(g.res, (int64_t)row * g.ld_res + nn[h] + j, g.res_f32, one);
-                        finish<LAY, DT>(g, e, row, nn[h] + j, v, bi, one);
+                        finish<LAY, DT>(g, e, split * g.c_split, row, nn[h] + j, v, bi, one);
                     }
                 }
             }
