@@ -51,8 +51,6 @@ int check_ws(void *ws, size_t have, size_t need) {
     return BITMOE_OK;
 }
 
-bool span32(int rows, int64_t ld) { return ld < (1 << 30) && rows * ld < ((int64_t)1 << 31); }
-
 // Division by an invariant: with 2^(s-1) < d <= 2^s, m = floor(2^(31+s) / d) + 1
 // gives floor(x / d) = floor(x m / 2^(31+s)) for every x < 2^31 (the excess
 // m d - 2^(31+s) is at most d <= 2^s, so x times it stays below 2^(31+s)).

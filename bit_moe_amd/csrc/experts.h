@@ -17,6 +17,9 @@ struct GemmRows {
     bool span32;               // the rows a tile may read together (all, by a map; else 256) span less than 4 GiB
 };
 
+// rows of a stride of ld 16-bit elements span less than 4 GiB
+inline bool span32(int rows, int64_t ld) { return ld < ((int64_t)1 << 31) && rows * ld < ((int64_t)1 << 31); }
+
 // C[m][n] = sum_k A[m][k] B[n][k] over the groups of rows that `offsets`
 // marks, in three layouts.
 enum GemmLayout {
@@ -45,6 +48,8 @@ struct GemmArgs {
     // rows in equal whole stages), each to its own C, c_split elements further
     int32_t splits, kper;
     int64_t c_split;
+    // kGradWeights with maps: the rows they give, or -1, of each of the call's
+    const int32_t *arows, *brows;
 };
 
 // How a product runs: which kernel, its tiles, into how many parts the
@@ -55,7 +60,7 @@ struct GemmPlan {
     int mt, nt;         // row tiles (of all groups, at most; kGradWeights: of an expert), column tiles
     int splits, kper;
     int64_t grid;       // workgroups that would take one tile each
-    size_t ws;
+    size_t ws;          // bytes: the parts' float32, then (kGradWeights) the rows of both maps
 };
 // every row begins on a 16-byte address and has whole 8-element pieces
 bool gemm_whole(int layout, const GemmArgs &g);

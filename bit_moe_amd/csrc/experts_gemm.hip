@@ -51,6 +51,15 @@ k_join(GemmArgs g, const float *part, int rows, int cshift) {
     }
 }
 
+// the rows that two operands' maps give
+__global__ void __launch_bounds__(256)
+k_rows(GemmRows a, GemmRows b, int R, int32_t *arows, int32_t *brows) {
+    const int r = blockIdx.x * 256 + threadIdx.x;
+    if (r >= R) return;
+    arows[r] = row_of(a, r);
+    brows[r] = row_of(b, r);
+}
+
 template <int LAY>
 int join(int dtype, const GemmArgs &g, const float *part, int rows, hipStream_t s) {
     const int per = (g.N + 7) / 8;
@@ -81,6 +90,16 @@ int launch_gemm(int layout, int dtype, const GemmArgs &args, void *ws, hipStream
     GemmArgs g = args;
     g.splits = p.splits;
     g.kper = p.kper;
+    if (layout == kGradWeights && (g.a.map || g.b.map) && p.kind != kAny && g.R > 0) {
+        const size_t each = ((size_t)g.R * 4 + 255) / 256 * 256;
+        int32_t *rows = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + p.ws - 2 * each);
+        k_rows<<<(g.R + 255) / 256, 256, 0, s>>>(g.a, g.b, g.R, rows, rows + each / 4);
+        BM_LAUNCH_CHECK();
+        g.arows = rows;
+        g.brows = rows + each / 4;
+        g.a.span32 = span32(g.a.rows, g.a.ld);
+        g.b.span32 = span32(g.b.rows, g.b.ld);
+    }
     if (p.splits == 1) return launch(layout, dtype, g, p, s);
     // the parts: plain float32 rows, joined by a second launch
     const int rows = layout == kGradWeights ? g.E * g.M : g.R;

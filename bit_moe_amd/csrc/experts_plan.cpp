@@ -73,6 +73,7 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
             }
         }
     }
+    if (layout == kGradWeights) best.ws += 2 * (((size_t)g.R * 4 + 255) / 256 * 256);
     return best;
 }
 

@@ -41,15 +41,18 @@ BM_DEV const uint16_t *wave_ptr(const uint16_t *p) {
 // (4 l).  In asm, because the compiler would wait for it before the next LDS
 // read, of whatever stage; phase_barrier() waits instead.
 BM_DEV void dma16(const void *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(src) : "memory");
 }
 // the same with a base of the wave's and 32-bit offsets (bytes) of the lanes':
 // no arithmetic per load
 BM_DEV void dma16_from(const void *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(off), "s"(base) : "memory");
 }
 BM_DEV void dma4(const void *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(src) : "memory");
 }
 // all but this wave's last N loads have arrived, its LDS reads are done, and
 // so for every wave of the workgroup
@@ -62,11 +65,11 @@ BM_DEV void phase_barrier() {
 // next; A's rows; for the weights' gradient a ring of row maps (64 of A's, 64 of
 // B's, four stages); the epilogue's part, which is its own, so that the next
 // tile's first stages can be on their way during it.
-template <int LAY, int BM, int BN, int WM, int WN>
+template <int LAY, int BM, int BN, int WM, int WN, bool MAPS>
 struct TileLds {
     static constexpr int rows = 2 * (BM + BN) * kBK * 2;
     static constexpr int maps = rows + 3 * BM * 4;
-    static constexpr int out = maps + (LAY == kGradWeights ? 4 * 128 * 4 : 0);
+    static constexpr int out = maps + (MAPS ? 4 * 128 * 4 : 0);
     static constexpr int bytes = out + WM * WN * epilogue_floats<BN / WN / 16>() * 4;
     static_assert(bytes <= 160 * 1024, "");
 };
@@ -102,14 +105,16 @@ BM_DEV s16x8 frag_at(uint32_t at, int i, int kk) {
 #endif
 }
 
-template <int LAY, int DT, int BM, int BN, int WM, int WN>
+// MAPS (weights' gradient): the operands' rows are g.arows and g.brows (span32
+// is then of the whole operands).
+template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS>
 __global__ void __launch_bounds__(64 * WM * WN)
 k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     constexpr int NW = WM * WN, UM = BM / 2, UN = BN / 2;                  // a unit's rows
     constexpr int PA = UM * kBK / 8 / (64 * NW), PB = UN * kBK / 8 / (64 * NW);   // a unit's loads per wave
     constexpr int TI = UM / WM / 16, TJ = UN / WN / 16;                    // 16 x 16 products of a wave in a quadrant
     constexpr bool AKC = LAY != kGradWeights, BKC = LAY == kForward;
-    constexpr bool kMaps = LAY == kGradWeights;
+    static_assert(LAY == kGradWeights || !MAPS, "");
     constexpr int kUA = UM * kBK, kUB = UN * kBK, kStage = 2 * (kUA + kUB);       // elements
     static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW, "");
     extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
@@ -134,7 +139,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     // stage, by addresses made one by one, with the zero piece for what is not
     // there.  Rows past the group, and columns past the matrix, read its last
     // row (first columns): their results are not stored.
-    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::rows);
+    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::rows);
     int *xrow = srow + 2 * BM;
     int m0, n0, kbeg, kend, split, stages, whole;  // whole: whole stages
     const uint16_t *A, *B, *abase, *bbase;         // the matrices; what stage 0 goes by
@@ -186,7 +191,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
                 for (int i = 0; i < PB; i++)
                     boff[h * PB + i] = (uint32_t)min(h * UN + br + i * kRowB, g.N - 1 - n0) * (uint32_t)g.b.ld * 2 + 16 * bc;
         } else {
-            if (!kMaps) bbase += (int64_t)kbeg * g.b.ld;
+            if (LAY == kGradRows) bbase += (int64_t)kbeg * g.b.ld;
             else if (!g.b.map) bbase += (int64_t)t.r0 * g.b.ld;
 #pragma unroll
             for (int i = 0; i < PB; i++) boff[i] = (br + i * kRowB) * (uint32_t)g.b.ld * 2;
@@ -200,27 +205,22 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         bbase = wave_ptr(bbase);
         set_rows<LAY, BM>(g, t, m0, tid, srow + par * BM);
     };
-    // The weights' gradient: the rows' maps, fetched two stages before the loads
-    // that go by them; a stage's rows are resolved at the operand's first unit
-    // and kept for its second.  Every wave fetches them all, to the same place
-    // (the same values), and so waits only for its own loads.
-    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::maps);
+    // MAPS: the rows that the maps give (g.arows, g.brows), fetched two stages
+    // before the loads that go by them; a stage's offsets are made at the
+    // operand's first unit and kept for its second.  Every wave fetches them
+    // all, to the same place (the same values), and so waits only for its own
+    // loads.
+    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::maps);
     const uint32_t maps_at = lds_addr(maps);
-    auto fetch_map = [&](const GemmRows &q, int s, int b) {
-        const int k = min(s * kBK + lane, kend - 1);
-        dma4(q.map ? static_cast<const void *>(q.map + t.r0 + k) : zero, maps_at + ((s & 3) * 128 + b * 64) * 4);
+    auto fetch_map = [&](const int32_t *rows, int s, int b) {
+        dma4(rows + t.r0 + min(s * kBK + lane, kend - 1), maps_at + ((s & 3) * 128 + b * 64) * 4);
     };
-    auto map_row = [&](const GemmRows &q, int b, int s, int k) {
+    // row k of a stage of the weights' gradient, or -1
+    auto map_row = [&](int b, int s, int k) {
         if (s * kBK + k >= kend) return -1;
-        int m = t.r0 + s * kBK + k;
-        if (q.map) {
-            m = maps[(s & 3) * 128 + b * 64 + k];
-            if (m < 0) return -1;
-            m = divided(q, m);
-        }
-        return m < q.rows ? m : -1;
+        return MAPS ? maps[(s & 3) * 128 + b * 64 + k] : t.r0 + s * kBK + k;
     };
-    bool awhole = false, bwhole = false;           // mapped rows of the stage being loaded: all there
+    bool awhole = false, bwhole = false;           // MAPS: the rows of the stage being loaded are all there
     const uint32_t lds0 = lds_addr(lds) + wave * 1024;
     // load i of A's (B's) half h of stage s (fast: by the base, but for maps)
     auto load_a = [&](auto fast, int s, int buf, int h, int i) {
@@ -230,10 +230,9 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             const int k = kbeg + s * kBK + 8 * ac, row = xrow[h * UM + ar + i * kRowA];
             dma16(k < kend && row >= 0 ? A + (int64_t)row * g.a.ld + k : zero, to);
         } else {
-            const bool mapped = g.a.map != nullptr;
-            if (mapped ? awhole : fast)
-                return dma16_from(mapped ? A : abase + (int64_t)s * kBK * g.a.ld, aoff[i] + aoff[PA + h], to);
-            const int row = map_row(g.a, 0, s, ar + i * kRowA);
+            if (MAPS ? awhole : (bool)fast)
+                return dma16_from(MAPS ? A : abase + (int64_t)s * kBK * g.a.ld, aoff[i] + aoff[PA + h], to);
+            const int row = map_row(0, s, ar + i * kRowA);
             dma16(row >= 0 ? A + (int64_t)row * g.a.ld + aoff[PA + h] / 2 : zero, to);
         }
     };
@@ -244,29 +243,25 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             const int k = kbeg + s * kBK + 8 * bc;
             dma16(k < kend ? B + (int64_t)min(n0 + h * UN + br + i * kRowB, g.N - 1) * g.b.ld + k : zero, to);
         } else {
-            const bool mapped = kMaps && g.b.map != nullptr;
-            if (mapped ? bwhole : fast)
-                return dma16_from(mapped ? B : bbase + (int64_t)s * kBK * g.b.ld, boff[i] + boff[PB + h], to);
+            if (MAPS ? bwhole : (bool)fast)
+                return dma16_from(MAPS ? B : bbase + (int64_t)s * kBK * g.b.ld, boff[i] + boff[PB + h], to);
             const int k = kbeg + s * kBK + br + i * kRowB;
-            const int row = kMaps ? map_row(g.b, 1, s, br + i * kRowB) : k < kend ? k : -1;
+            const int row = LAY == kGradWeights ? map_row(1, s, br + i * kRowB) : k < kend ? k : -1;
             dma16(row >= 0 ? B + (int64_t)row * g.b.ld + boff[PB + h] / 2 : zero, to);
         }
     };
     // what the unit of phase p of stage s needs before its loads
     auto ready = [&](int s, int p) {
-        if (!kMaps || p > 1) return;
-        const GemmRows &q = p == 0 ? g.a : g.b;
-        if (q.map) {
-            bool there = true;
+        if (!MAPS || p > 1) return;
+        bool there = true;
 #pragma unroll
-            for (int i = 0; i < (p == 0 ? PA : PB); i++) {
-                const int row = map_row(q, p, s, p == 0 ? ar + i * kRowA : br + i * kRowB);
-                there = there && row >= 0;
-                (p == 0 ? aoff[i] : boff[i]) = (uint32_t)row * (uint32_t)q.ld * 2;
-            }
-            (p == 0 ? awhole : bwhole) = (p == 0 ? afast : bfast) && __all(there);
+        for (int i = 0; i < (p == 0 ? PA : PB); i++) {
+            const int row = map_row(p, s, p == 0 ? ar + i * kRowA : br + i * kRowB);
+            there = there && row >= 0;
+            (p == 0 ? aoff[i] : boff[i]) = (uint32_t)row * (uint32_t)(p == 0 ? g.a.ld : g.b.ld) * 2;
         }
-        fetch_map(q, s + 2, p);
+        (p == 0 ? awhole : bwhole) = (p == 0 ? afast : bfast) && __all(there);
+        fetch_map(p == 0 ? g.arows : g.brows, s + 2, p);
     };
     // the loads of phase p for stage s, of parity f: its place in LDS, and B's
     // half that comes first
@@ -301,7 +296,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
                 acc[ih * TI + i][jh * TJ + j] = mfma16<DT>(b[kk][j], a[kk][i], acc[ih * TI + i][jh * TJ + j]);
     };
     // loads issued after the ones a phase waits for (the maps' among them)
-    constexpr int kWait3 = 2 * PA + 3 * PB + 2 * kMaps, kWait0 = 3 * PA + 2 * PB + 2 * kMaps;
+    constexpr int kWait3 = 2 * PA + 3 * PB + 2 * MAPS, kWait0 = 3 * PA + 2 * PB + 2 * MAPS;
     // stage s of parity f, whose first B half is f: in rbf on entry, with A0 in ra0
     auto stage = [&](auto fast, int s, int f, s16x8 (&rbf)[2][TJ], s16x8 (&rbs)[2][TJ]) {
 #pragma unroll
@@ -332,10 +327,10 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     // the loads of a tile's first two stages
     auto begin = [&]() {
         if (stages == 0) return;
-        if (kMaps) {
+        if (MAPS) {
             for (int s = 0; s < 4; s++) {
-                fetch_map(g.a, s, 0);
-                fetch_map(g.b, s, 1);
+                fetch_map(g.arows, s, 0);
+                fetch_map(g.brows, s, 1);
             }
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
@@ -349,7 +344,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
                     for (int i = 0; i < kLoads; i++) load(fast, s, s, p, i);
                 }
         };
-        if (afast && bfast && whole >= 2) both(std::true_type{});
+        if (!MAPS && afast && bfast && whole >= 2) both(std::true_type{});
         else both(std::false_type{});
     };
     // a tile that is there
@@ -369,14 +364,14 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
 #pragma unroll
             for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (stages > 0) {
-            phase_barrier<3 * PA + 3 * PB + 2 * kMaps>();
+            phase_barrier<3 * PA + 3 * PB + 2 * MAPS>();
 #pragma unroll
             for (int kk = 0; kk < 2; kk++) {
                 read_a(0, 0, kk, ra0);
                 read_b(0, 0, kk, rb0);
             }
             int s = 0;
-            if ((afast || (kMaps && g.a.map)) && (bfast || (kMaps && g.b.map)))
+            if (!MAPS && afast && bfast)
                 for (; s + 3 < whole; s += 2) {
                     stage(std::true_type{}, s, 0, rb0, rb1);
                     stage(std::true_type{}, s + 1, 1, rb1, rb0);
@@ -396,7 +391,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         __syncthreads();       // xrow; srow, where no stage was
         if (more) begin();
         tile_epilogue<LAY, DT, BM, BN, 2>(
-            g, acc, reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN>::out),
+            g, acc, reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::out),
             srow + par * BM, e, part, n, wm * (UM / WM), wn * (UN / WN), wave, lane);
         if (!more) return;
     }
