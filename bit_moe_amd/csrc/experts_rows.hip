@@ -3,6 +3,7 @@
 // All are bound by memory: each thread takes 8 consecutive values (16 bytes)
 // of a row, reads every operand once and computes in fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_util.h"
 
@@ -11,7 +12,9 @@ namespace {
 using namespace bm;
 
 // A block's 256 threads over the rows' 8-value pieces: 2^cshift of them along
-// a row (at least one row's pieces, or 256), the rest over further rows.
+// a row, the rest over further rows.  Of 256, 128 and 64 the widest that leaves
+// no more than a sixteenth of the threads without a piece (7168 values are 3.5
+// times 256 pieces, 7 times 128).
 struct Grid2 {
     dim3 grid;
     int cshift;
@@ -20,51 +23,86 @@ Grid2 pieces_grid(int rows, int cols) {
     const int per = (cols + 7) / 8;
     int cs = 0;
     while (cs < 8 && (1 << cs) < per) cs++;
+    auto idle = [&](int c) { return (((per + (1 << c) - 1) >> c) << c) - per; };
+    int best = cs;
+    for (int c = cs; c >= 6 && idle(best) * 16 > per; c--)
+        if (idle(c) < idle(best)) best = c;
+    cs = best;
     const int rpb = 256 >> cs;
     return {dim3((per + (1 << cs) - 1) >> cs, std::min((rows + rpb - 1) / rpb, 65535)), cs};
 }
-#define BM_FOR_PIECES(r, c, rows, cols, cshift)                                                   \
-    const int c = ((blockIdx.x << cshift) + (threadIdx.x & ((1 << cshift) - 1))) * 8;             \
-    if (c < cols)                                                                                 \
-        for (int r = blockIdx.y * (256 >> cshift) + (threadIdx.x >> cshift); r < rows; r += gridDim.y * (256 >> cshift))
+// body(full, row, column) for each piece: full is a constant, true where all 8
+// values are there, so that a piece's loads are issued together, not each
+// behind a test (which cost the combine a quarter of its rate).
+template <class F>
+BM_DEV void for_pieces(int rows, int cols, int cshift, F body) {
+    const int c = ((blockIdx.x << cshift) + (threadIdx.x & ((1 << cshift) - 1))) * 8;
+    const int step = gridDim.y * (256 >> cshift);
+    int r = blockIdx.y * (256 >> cshift) + (threadIdx.x >> cshift);
+    if (c + 8 <= cols) {
+        for (; r < rows; r += step) body(std::true_type{}, r, c);
+    } else if (c < cols) {
+        for (; r < rows; r += step) body(std::false_type{}, r, c);
+    }
+}
 
 struct Mat {
     void *p;
     int64_t ld;
 };
+// a piece as it is in memory, and its values
+template <bool FULL>
+BM_DEV uint4 piece(const Mat &m, int64_t r, int c, int cols) {
+    const uint16_t *p = static_cast<const uint16_t *>(m.p) + r * m.ld + c;
+    return FULL ? load16(p) : load16_part(p, cols - c);
+}
+template <int DT>
+BM_DEV void values(const uint4 &u, float *v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = elem_f32<DT>(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu);
+}
+template <int DT, bool FULL>
+BM_DEV void put(const Mat &m, int64_t r, int c, int cols, bool f32, const float *v) {
+    store8<DT>(m.p, r * m.ld + c, FULL ? 8 : cols - c, f32, v);
+}
 
 // h = silu(gate) up
 template <int DT>
 __global__ void __launch_bounds__(256)
 k_swiglu(Mat gate, Mat up, Mat h, int R, int I, int cshift) {
-    BM_FOR_PIECES(r, c, R, I, cshift) {
+    for_pieces(R, I, cshift, [&](auto whole, int r, int c) {
+        constexpr bool full = decltype(whole)::value;
         float a[8], b[8];
-        load8<DT>(gate.p, (int64_t)r * gate.ld + c, I - c, false, a);
-        load8<DT>(up.p, (int64_t)r * up.ld + c, I - c, false, b);
+        const uint4 ua = piece<full>(gate, r, c, I), ub = piece<full>(up, r, c, I);
+        values<DT>(ua, a);
+        values<DT>(ub, b);
 #pragma unroll
         for (int j = 0; j < 8; j++) a[j] = silu(a[j]) * b[j];
-        store8<DT>(h.p, (int64_t)r * h.ld + c, I - c, false, a);
-    }
+        put<DT, full>(h, r, c, I, false, a);
+    });
 }
 
 // with p = 1 / (1 + e^-gate): dgate = dh up p (1 + gate (1 - p)), dup = dh gate p
 template <int DT>
 __global__ void __launch_bounds__(256)
 k_swiglu_backward(Mat dh, Mat gate, Mat up, Mat dgate, Mat dup, int R, int I, int cshift) {
-    BM_FOR_PIECES(r, c, R, I, cshift) {
+    for_pieces(R, I, cshift, [&](auto whole, int r, int c) {
+        constexpr bool full = decltype(whole)::value;
         float d[8], a[8], b[8];
-        load8<DT>(dh.p, (int64_t)r * dh.ld + c, I - c, false, d);
-        load8<DT>(gate.p, (int64_t)r * gate.ld + c, I - c, false, a);
-        load8<DT>(up.p, (int64_t)r * up.ld + c, I - c, false, b);
+        const uint4 ud = piece<full>(dh, r, c, I), ua = piece<full>(gate, r, c, I), ub = piece<full>(up, r, c, I);
+        values<DT>(ud, d);
+        values<DT>(ua, a);
+        values<DT>(ub, b);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const float p = 1.f / (1.f + __expf(-a[j])), g = a[j];
             a[j] = d[j] * b[j] * p * (1.f + g * (1.f - p));
             b[j] = d[j] * g * p;
         }
-        store8<DT>(dgate.p, (int64_t)r * dgate.ld + c, I - c, false, a);
-        store8<DT>(dup.p, (int64_t)r * dup.ld + c, I - c, false, b);
-    }
+        put<DT, full>(dgate, r, c, I, false, a);
+        put<DT, full>(dup, r, c, I, false, b);
+    });
 }
 
 // y[t] = sum_j w[t][j] o[t k + j] + residual[t], j ascending; KM >= k rows are
@@ -72,28 +110,32 @@ k_swiglu_backward(Mat dh, Mat gate, Mat up, Mat dgate, Mat dup, int R, int I, in
 template <int DT, int KM>
 __global__ void __launch_bounds__(256)
 k_combine(Mat o, const float *w, int T, int k, int H, Mat res, bool res_f32, Mat y, bool y_f32, int cshift) {
-    BM_FOR_PIECES(t, c, T, H, cshift) {
-        float v[KM][8], acc[8];
+    for_pieces(T, H, cshift, [&](auto whole, int t, int c) {
+        constexpr bool full = decltype(whole)::value;
+        uint4 u[KM];
+        float wt[KM], acc[8], q[8];
 #pragma unroll
         for (int j = 0; j < KM; j++)
-            if (j < k) load8<DT>(o.p, ((int64_t)t * k + j) * o.ld + c, H - c, false, v[j]);
+            if (j < k) u[j] = piece<full>(o, (int64_t)t * k + j, c, H);
+#pragma unroll
+        for (int j = 0; j < KM; j++) wt[j] = w && j < k ? w[(int64_t)t * k + j] : 1.f;
+        if (res.p) load8<DT>(res.p, (int64_t)t * res.ld + c, full ? 8 : H - c, res_f32, q);
 #pragma unroll
         for (int i = 0; i < 8; i++) acc[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < KM; j++)
             if (j < k) {
-                const float wj = w ? w[(int64_t)t * k + j] : 1.f;
+                float v[8];
+                values<DT>(u[j], v);
 #pragma unroll
-                for (int i = 0; i < 8; i++) acc[i] = fmaf(wj, v[j][i], acc[i]);
+                for (int i = 0; i < 8; i++) acc[i] = fmaf(wt[j], v[i], acc[i]);
             }
         if (res.p) {
-            float q[8];
-            load8<DT>(res.p, (int64_t)t * res.ld + c, H - c, res_f32, q);
 #pragma unroll
             for (int i = 0; i < 8; i++) acc[i] += q[i];
         }
-        store8<DT>(y.p, (int64_t)t * y.ld + c, H - c, y_f32, acc);
-    }
+        put<DT, full>(y, t, c, H, y_f32, acc);
+    });
 }
 
 // One workgroup per token: d_o[t k + j] = w[t][j] dy[t] and, summed over the
@@ -110,29 +152,41 @@ k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int T, int k, int
         wt[j] = w && j < k ? w[(int64_t)t * k + j] : 1.f;
         dot[j] = 0.f;
     }
-    for (int c = tid * 8; c < H; c += blockDim.x * 8) {
-        float d[8], v[KM][8];
-        load8<DT>(dy.p, (int64_t)t * dy.ld + c, H - c, dy_f32, d);
+    auto at = [&](auto whole, int c) {
+        constexpr bool full = decltype(whole)::value;
+        float d[8];
+        uint4 u[KM];
         if (dw) {
 #pragma unroll
             for (int j = 0; j < KM; j++)
-                if (j < k) load8<DT>(o.p, ((int64_t)t * k + j) * o.ld + c, H - c, false, v[j]);
-#pragma unroll
-            for (int j = 0; j < KM; j++)
-                if (j < k)
-#pragma unroll
-                    for (int i = 0; i < 8; i++) dot[j] = fmaf(d[i], v[j][i], dot[j]);
+                if (j < k) u[j] = piece<full>(o, (int64_t)t * k + j, c, H);
         }
+        load8<DT>(dy.p, (int64_t)t * dy.ld + c, full ? 8 : H - c, dy_f32, d);
         if (d_o.p) {
+            // (o is read: d_o may be o)
 #pragma unroll
             for (int j = 0; j < KM; j++)
                 if (j < k) {
                     float q[8];
 #pragma unroll
                     for (int i = 0; i < 8; i++) q[i] = wt[j] * d[i];
-                    store8<DT>(d_o.p, ((int64_t)t * k + j) * d_o.ld + c, H - c, false, q);
+                    put<DT, full>(d_o, (int64_t)t * k + j, c, H, false, q);
                 }
         }
+        if (dw) {
+#pragma unroll
+            for (int j = 0; j < KM; j++)
+                if (j < k) {
+                    float v[8];
+                    values<DT>(u[j], v);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) dot[j] = fmaf(d[i], v[i], dot[j]);
+                }
+        }
+    };
+    for (int c = tid * 8; c < H; c += blockDim.x * 8) {
+        if (c + 8 <= H) at(std::true_type{}, c);
+        else at(std::false_type{}, c);
     }
     if (!dw) return;
 #pragma unroll
@@ -157,21 +211,27 @@ k_act_backward(bm_host::ActBackward p, int rows_per, int want_sum) {
     __shared__ float red[8][256];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 256 + tx * 8;
     const int r0 = blockIdx.y * rows_per, r1 = min(r0 + rows_per, p.T);
+    const Mat dy{const_cast<void *>(p.dy), p.ld_dy}, pre{const_cast<void *>(p.pre), p.ld_pre}, dz{p.dz, p.ld_dz};
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < p.N)
-        for (int r = r0 + ty; r < r1; r += 8) {
-            float d[8];
-            load8<DT>(p.dy, (int64_t)r * p.ld_dy + c, p.N - c, false, d);
-            if (p.pre) {
-                float z[8];
-                load8<DT>(p.pre, (int64_t)r * p.ld_pre + c, p.N - c, false, z);
-#pragma unroll
-                for (int j = 0; j < 8; j++) d[j] *= act_slope(z[j], p.act);
-            }
-            if (p.dz) store8<DT>(p.dz, (int64_t)r * p.ld_dz + c, p.N - c, false, d);
-#pragma unroll
-            for (int j = 0; j < 8; j++) sum[j] += d[j];
+    auto at = [&](auto whole, int r) {
+        constexpr bool full = decltype(whole)::value;
+        float d[8], z[8];
+        const uint4 ud = piece<full>(dy, r, c, p.N), uz = p.pre ? piece<full>(pre, r, c, p.N) : make_uint4(0, 0, 0, 0);
+        values<DT>(ud, d);
+        if (p.pre) {
+            values<DT>(uz, z);
+            slope_row(d, z, p.act);
         }
+        if (p.dz) put<DT, full>(dz, r, c, p.N, false, d);
+#pragma unroll
+        for (int j = 0; j < 8; j++) sum[j] += d[j];
+    };
+    if (c + 8 <= p.N) {
+#pragma unroll 2
+        for (int r = r0 + ty; r < r1; r += 8) at(std::true_type{}, r);
+    } else if (c < p.N) {
+        for (int r = r0 + ty; r < r1; r += 8) at(std::false_type{}, r);
+    }
     if (!want_sum) return;
 #pragma unroll
     for (int j = 0; j < 8; j++) red[ty][tx * 8 + j] = sum[j];
@@ -190,8 +250,16 @@ k_bias_grad(const float *partial, int slices, int N, void *db, int db_dtype) {
     __shared__ float red[16][16];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = blockIdx.x * 16 + tx;
     float s = 0.f;
-    if (c < N)
-        for (int i = ty; i < slices; i += 16) s += partial[(int64_t)i * N + c];
+    if (c < N) {
+        // eight at a time: one round trip to memory for 128 slices
+        for (int i0 = ty; i0 < slices; i0 += 128) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = i0 + 16 * j < slices ? partial[(int64_t)(i0 + 16 * j) * N + c] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; j++) s += v[j];
+        }
+    }
     red[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && c < N) {
@@ -260,6 +328,7 @@ int launch_swiglu_backward(const bitmoe_rows &dh, const bitmoe_rows &gate, const
 int launch_combine(const bitmoe_rows &o, const float *w, int T, int k, const bitmoe_rows *residual,
                    const bitmoe_rows &y, hipStream_t s) {
     if (k <= 2) return combine_k<2>(o, w, T, k, residual, y, s);
+    if (k <= 4) return combine_k<4>(o, w, T, k, residual, y, s);
     if (k <= 8) return combine_k<8>(o, w, T, k, residual, y, s);
     return combine_k<16>(o, w, T, k, residual, y, s);
 }
@@ -267,6 +336,7 @@ int launch_combine(const bitmoe_rows &o, const float *w, int T, int k, const bit
 int launch_combine_backward(const bitmoe_rows &dy, const bitmoe_rows *o, const float *w, int T, int k,
                             const bitmoe_rows *d_o, float *dw, int dtype, hipStream_t s) {
     if (k <= 2) return combine_backward_k<2>(dy, o, w, T, k, d_o, dw, dtype, s);
+    if (k <= 4) return combine_backward_k<4>(dy, o, w, T, k, d_o, dw, dtype, s);
     if (k <= 8) return combine_backward_k<8>(dy, o, w, T, k, d_o, dw, dtype, s);
     return combine_backward_k<16>(dy, o, w, T, k, d_o, dw, dtype, s);
 }

@@ -358,6 +358,20 @@ BM_DEV float act_slope(float z, int act) {
     }
 }
 
+BM_DEV void slope_row(float (&d)[8], const float (&z)[8], int act) {
+#define BM_SLOPE(A)                                                                     \
+    case A:                                                                             \
+        _Pragma("unroll") for (int j = 0; j < 8; j++) d[j] *= act_slope(z[j], A);       \
+        break;
+    switch (act) {
+        BM_SLOPE(BITMOE_ACT_RELU)
+        BM_SLOPE(BITMOE_ACT_GELU)
+        BM_SLOPE(BITMOE_ACT_GELU_TANH)
+        BM_SLOPE(BITMOE_ACT_SILU)
+    }
+#undef BM_SLOPE
+}
+
 // Eight (W = 8) outputs of a row, or the one at the edge (W = 1): n.. of row
 // `row` of the output, with the bias's and the residual's values;
 // part: where a part of a split begins.

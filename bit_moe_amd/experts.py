@@ -18,52 +18,71 @@ ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 MATMUL, MATMUL_DX, MATMUL_DW = 0, 1, 2
 
 
-def _dtype(t, what, f32=False):
+def _codes():
     torch = _torch()
-    code = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}.get(t.dtype)
+    return {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+
+
+_DTYPES = None
+
+
+def _dtype(t, what, f32=False):
+    global _DTYPES
+    if _DTYPES is None:
+        _DTYPES = _codes()
+    code = _DTYPES.get(t.dtype)
     if code is None or (code == F32 and not f32):
         raise TypeError(f"{what} must be bfloat16 or float16" + (" or float32" if f32 else ""))
     return code
 
 
-def _ld(t, dim=-2):
-    """Elements between rows; a single row has no stride of its own."""
-    return t.stride(dim) if t.shape[dim] > 1 else max(t.stride(dim), t.shape[-1])
-
-
-def _matrix(t, dims, what):
-    if t.dim() != dims:
-        raise ValueError(f"{what} must have {dims} dimensions")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+def _strided(shape, stride, what):
+    """Elements between rows of a matrix (the last two dimensions)."""
+    n, cols = shape[-2], shape[-1]
+    if n == 0 or cols == 0:
+        return cols
+    if cols > 1 and stride[-1] != 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
-    # (rows that overlap, as an expanded tensor's do, are refused)
-    if t.numel() and t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
-        raise ValueError(f"{what} must have rows that do not overlap")
-    return t
+    ld = stride[-2]
+    if ld < cols:
+        # (a single row has no stride of its own; rows that overlap, as an expanded tensor's do, are refused)
+        if n > 1:
+            raise ValueError(f"{what} must have rows that do not overlap")
+        ld = cols
+    return ld
 
 
 def _rows(t, what, rows_map=None, div=1, f32=False):
-    _matrix(t, 2, what)
-    n, cols = t.shape
-    return RowsStruct(t.data_ptr(), None if rows_map is None else rows_map.data_ptr(), max(_ld(t), cols), n, cols, div,
-                      _dtype(t, what, f32))
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have 2 dimensions")
+    return RowsStruct(t.data_ptr(), None if rows_map is None else rows_map.data_ptr(),
+                      _strided(shape, t.stride(), what), shape[0], shape[1], div, _dtype(t, what, f32))
 
 
 def _experts(t, what, f32=False):
-    _matrix(t, 3, what)
-    E, N, K = t.shape
-    ld = max(_ld(t), K)
-    return ExpertsStruct(t.data_ptr(), ld, t.stride(0) if E > 1 else N * ld, E, N, K, _dtype(t, what, f32))
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have 3 dimensions")
+    E, N, K = shape
+    ld = _strided(shape, stride, what)
+    return ExpertsStruct(t.data_ptr(), ld, stride[0] if E > 1 else N * ld, E, N, K, _dtype(t, what, f32))
+
+
+def _one(t, what, f32=False):
+    """A matrix as a single expert's."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have 2 dimensions")
+    ld = _strided(shape, t.stride(), what)
+    return ExpertsStruct(t.data_ptr(), ld, shape[0] * ld, 1, shape[0], shape[1], _dtype(t, what, f32))
 
 
 def _ints(t, what, n=None):
-    torch = _torch()
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_cuda or (t.numel() > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous one-dimensional int32 tensor on the GPU")
+    if t.dtype != _torch().int32 or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous one-dimensional int32 tensor")
     if n is not None and t.numel() != n:
         raise ValueError(f"{what} must have {n} elements")
     return t
@@ -77,17 +96,23 @@ def _count(x, x_rows, y_rows, *names):
     return n[0] if n else x.shape[0]
 
 
-def _one_device(*ts):
-    dev = None
+def _device(*ts):
+    """The index of the tensors' one device."""
+    dev = ts[0].get_device()
     for t in ts:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError("tensors must be on the GPU")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError("tensors must be on one device")
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one device")
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
     return dev
+
+
+def _current_stream(dev):
+    """The current stream's handle (without a torch.cuda.Stream object, where
+    torch offers that: 1 us less per call)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _run(dev, stream, call):
@@ -95,23 +120,26 @@ def _run(dev, stream, call):
     stream, that stream current, so that what call allocates lives on it."""
     torch = _torch()
     if stream is not None:
-        if stream.device != dev:
+        if stream.device.index != dev:
             raise ValueError("the stream must be on the tensors' device")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+    if dev == torch.cuda.current_device():
+        return call(_current_stream(dev))
     with torch.cuda.device(dev):
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _scratch(ws, need, dev):
+    """(the tensor, its address, its bytes)"""
     torch = _torch()
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     elif not ws.is_contiguous() or ws.dtype != torch.uint8:
         raise ValueError("ws must be a contiguous uint8 tensor")
-    return (ws, ws.data_ptr(), ws.numel()) if ws is not None else (None, None, 0)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def expert_matmul_workspace_bytes(op: int, E: int, R: int, N: int, K: int) -> int:
@@ -123,7 +151,7 @@ def expert_matmul_workspace_bytes(op: int, E: int, R: int, N: int, K: int) -> in
 def _expert_rows(fn, op, a, w, offsets, a_rows, a_div, c_rows, c, out_dtype, ws, stream, names):
     torch = _torch()
     an, cn = names
-    dev = _one_device(a, w, offsets, a_rows, c_rows, c, ws)
+    dev = _device(a, w, offsets, a_rows, c_rows, c, ws)
     _ints(a_rows, f"{an}_rows")
     _ints(c_rows, f"{cn}_rows")
     R = _count(a, a_rows, c_rows, f"{an}_rows", f"{cn}_rows")
@@ -177,7 +205,7 @@ def expert_matmul_dw(dy, x, offsets, dy_rows=None, dy_div=1, x_rows=None, x_div=
     expert_matmul's w: dw [E, N, K] (0 for an expert without rows; added to
     what dw holds if accumulate); maps as in expert_matmul."""
     torch = _torch()
-    dev = _one_device(dy, x, offsets, dy_rows, x_rows, dw, ws)
+    dev = _device(dy, x, offsets, dy_rows, x_rows, dw, ws)
     _ints(dy_rows, "dy_rows")
     _ints(x_rows, "x_rows")
     n = [t.shape[0] if m is None else m.numel() for t, m in ((dy, dy_rows), (x, x_rows))]
@@ -224,8 +252,8 @@ def linear(x, w, bias=None, act="none", residual=None, keep_pre=False, y=None, p
     None.  y may be the residual itself."""
     torch = _torch()
     code = _act(act)
-    dev = _one_device(x, w, bias, residual, y, pre, ws)
-    we = _experts(_matrix(w, 2, "w").unsqueeze(0), "w")
+    dev = _device(x, w, bias, residual, y, pre, ws)
+    we = _one(w, "w")
     xr = _rows(x, "x")
     T, N = x.shape[0], we.N
     if xr.cols != we.K or x.dtype != w.dtype:
@@ -263,8 +291,8 @@ def linear_backward(dy, x, w, act="none", pre=None, dx=None, dw=None, db=None, n
     code = _act(act)
     if code and pre is None:
         raise ValueError("pre is needed with an activation")
-    dev = _one_device(dy, x, w, pre, dx, dw, db, ws)
-    we = _experts(_matrix(w, 2, "w").unsqueeze(0), "w")
+    dev = _device(dy, x, w, pre, dx, dw, db, ws)
+    we = _one(w, "w")
     T, N, K = dy.shape[0], we.N, we.K
     for t, shape, name in ((dy, (T, N), "dy"), (x, (T, K), "x"), (pre if code else None, (T, N), "pre"),
                            (dx, (T, K), "dx"), (dw, (N, K), "dw"), (db, (N,), "db")):
@@ -286,7 +314,7 @@ def linear_backward(dy, x, w, act="none", pre=None, dx=None, dw=None, db=None, n
         if db is None and need_db:
             db = torch.empty((N,), dtype=dt, device=dev)
         dxr = None if dx is None else _rows(dx, "dx", f32=True)
-        dwe = None if dw is None else _experts(_matrix(dw, 2, "dw").unsqueeze(0), "dw", f32=True)
+        dwe = None if dw is None else _one(dw, "dw", f32=True)
         scratch, p, n = _scratch(ws, int(lib().moe_linear_backward_workspace_bytes(T, N, K)), dev)
         _check(lib().moe_linear_backward(C.byref(dyr), C.byref(xr), C.byref(we), code, _ref(pr), _ref(dxr), _ref(dwe),
                                          None if db is None else db.data_ptr(),
@@ -300,7 +328,7 @@ def swiglu(gate, up, h=None, stream=None):
     """h = silu(gate) * up, all [R, I] with any row stride (gate and up may be
     the halves of one product's output).  h may be gate or up."""
     torch = _torch()
-    dev = _one_device(gate, up, h)
+    dev = _device(gate, up, h)
     g, u = _rows(gate, "gate"), _rows(up, "up")
 
     def call(s):
@@ -318,7 +346,7 @@ def swiglu_backward(dh, gate, up, dgate=None, dup=None, stream=None):
     """Gradients of swiglu: (dgate, dup).  Without them given, both are views
     of one new [R, 2 I] matrix, gate's half first."""
     torch = _torch()
-    dev = _one_device(dh, gate, up, dgate, dup)
+    dev = _device(dh, gate, up, dgate, dup)
     if (dgate is None) != (dup is None):
         raise ValueError("dgate and dup are given together")
     d, g, u = _rows(dh, "dh"), _rows(gate, "gate"), _rows(up, "up")
@@ -337,8 +365,10 @@ def swiglu_backward(dh, gate, up, dgate=None, dup=None, stream=None):
 
 
 def _same(ts, names):
-    if any(t.shape != ts[0].shape or t.dtype != ts[0].dtype for t in ts):
-        raise ValueError(f"{names} must be of one shape and type")
+    shape, dtype = ts[0].shape, ts[0].dtype
+    for t in ts:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{names} must be of one shape and type")
 
 
 def _weights(w, k, n, what):
@@ -364,7 +394,7 @@ def combine(o, w=None, k=None, residual=None, y=None, out_dtype=None, stream=Non
     y [T, H] in out_dtype (default the residual's, else o's; o's or float32); y
     may be the residual itself."""
     torch = _torch()
-    dev = _one_device(o, w, residual, y)
+    dev = _device(o, w, residual, y)
     T, k = _weights(w, k, o.shape[0], "o")
     orow = _rows(o, "o")
     rr = None if residual is None else _rows(residual, "residual", f32=True)
@@ -396,7 +426,7 @@ def combine_backward(dy, o=None, w=None, k=None, d_o=None, dw=None, need_do=True
     need_do = need_do or d_o is not None
     if need_dw and o is None:
         raise ValueError("dw needs o")
-    dev = _one_device(dy, o, w, d_o, dw)
+    dev = _device(dy, o, w, d_o, dw)
     if o is None and w is None and k is None:
         raise ValueError("without o and w, k is needed")
     n = o.shape[0] if o is not None else dy.shape[0] * (w.shape[1] if w is not None else k)
