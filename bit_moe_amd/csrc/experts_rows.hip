@@ -50,11 +50,26 @@ struct Mat {
     void *p;
     int64_t ld;
 };
+// Whether a call's operands go through the memory-side cache (256 MiB), as
+// they should where the kernel before left them there or the next will read
+// them, or past it: loads past it from 288 MiB moved (combine of k 8, H 7168:
+// 44.2 us, 45.9 past it, at 280 MiB; 109 and 88 at 560; swiglu 29.1 and 32.9 at
+// 192 MiB, 138 and 116 at 768), stores too from 768 MiB (combine's backward 86
+// us with stores through it, 102 past it, at 448 MiB moved; 203 and 187 at 896).
+enum { kCached, kLoadsPast, kAllPast };
+int past_cache(int64_t bytes) {
+    return bytes >= (int64_t)768 << 20 ? kAllPast : bytes >= (int64_t)288 << 20 ? kLoadsPast : kCached;
+}
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // a piece as it is in memory, and its values
-template <bool FULL>
+template <bool FULL, int PAST>
 BM_DEV uint4 piece(const Mat &m, int64_t r, int c, int cols) {
     const uint16_t *p = static_cast<const uint16_t *>(m.p) + r * m.ld + c;
-    return FULL ? load16(p) : load16_part(p, cols - c);
+    if (!FULL) return load16_part(p, cols - c);
+    if (PAST == kCached) return load16(p);
+    const u32x4_any u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 template <int DT>
 BM_DEV void values(const uint4 &u, float *v) {
@@ -62,35 +77,42 @@ BM_DEV void values(const uint4 &u, float *v) {
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] = elem_f32<DT>(w[j >> 1] >> (16 * (j & 1)) & 0xFFFFu);
 }
-template <int DT, bool FULL>
+template <int DT, bool FULL, int PAST>
 BM_DEV void put(const Mat &m, int64_t r, int c, int cols, bool f32, const float *v) {
+    if (FULL && PAST == kAllPast && !f32) {
+        u32x4_any u;
+#pragma unroll
+        for (int j = 0; j < 4; j++) u[j] = elem_pair<DT>(v[2 * j], v[2 * j + 1]);
+        __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(m.p) + r * m.ld + c));
+        return;
+    }
     store8<DT>(m.p, r * m.ld + c, FULL ? 8 : cols - c, f32, v);
 }
 
 // h = silu(gate) up
-template <int DT>
+template <int DT, int PAST>
 __global__ void __launch_bounds__(256)
 k_swiglu(Mat gate, Mat up, Mat h, int R, int I, int cshift) {
     for_pieces(R, I, cshift, [&](auto whole, int r, int c) {
         constexpr bool full = decltype(whole)::value;
         float a[8], b[8];
-        const uint4 ua = piece<full>(gate, r, c, I), ub = piece<full>(up, r, c, I);
+        const uint4 ua = piece<full, PAST>(gate, r, c, I), ub = piece<full, PAST>(up, r, c, I);
         values<DT>(ua, a);
         values<DT>(ub, b);
 #pragma unroll
         for (int j = 0; j < 8; j++) a[j] = silu(a[j]) * b[j];
-        put<DT, full>(h, r, c, I, false, a);
+        put<DT, full, PAST>(h, r, c, I, false, a);
     });
 }
 
 // with p = 1 / (1 + e^-gate): dgate = dh up p (1 + gate (1 - p)), dup = dh gate p
-template <int DT>
+template <int DT, int PAST>
 __global__ void __launch_bounds__(256)
 k_swiglu_backward(Mat dh, Mat gate, Mat up, Mat dgate, Mat dup, int R, int I, int cshift) {
     for_pieces(R, I, cshift, [&](auto whole, int r, int c) {
         constexpr bool full = decltype(whole)::value;
         float d[8], a[8], b[8];
-        const uint4 ud = piece<full>(dh, r, c, I), ua = piece<full>(gate, r, c, I), ub = piece<full>(up, r, c, I);
+        const uint4 ud = piece<full, PAST>(dh, r, c, I), ua = piece<full, PAST>(gate, r, c, I), ub = piece<full, PAST>(up, r, c, I);
         values<DT>(ud, d);
         values<DT>(ua, a);
         values<DT>(ub, b);
@@ -100,14 +122,14 @@ k_swiglu_backward(Mat dh, Mat gate, Mat up, Mat dgate, Mat dup, int R, int I, in
             a[j] = d[j] * b[j] * p * (1.f + g * (1.f - p));
             b[j] = d[j] * g * p;
         }
-        put<DT, full>(dgate, r, c, I, false, a);
-        put<DT, full>(dup, r, c, I, false, b);
+        put<DT, full, PAST>(dgate, r, c, I, false, a);
+        put<DT, full, PAST>(dup, r, c, I, false, b);
     });
 }
 
 // y[t] = sum_j w[t][j] o[t k + j] + residual[t], j ascending; KM >= k rows are
 // loaded together
-template <int DT, int KM>
+template <int DT, int KM, int PAST>
 __global__ void __launch_bounds__(256)
 k_combine(Mat o, const float *w, int T, int k, int H, Mat res, bool res_f32, Mat y, bool y_f32, int cshift) {
     for_pieces(T, H, cshift, [&](auto whole, int t, int c) {
@@ -116,7 +138,7 @@ k_combine(Mat o, const float *w, int T, int k, int H, Mat res, bool res_f32, Mat
         float wt[KM], acc[8], q[8];
 #pragma unroll
         for (int j = 0; j < KM; j++)
-            if (j < k) u[j] = piece<full>(o, (int64_t)t * k + j, c, H);
+            if (j < k) u[j] = piece<full, PAST>(o, (int64_t)t * k + j, c, H);
 #pragma unroll
         for (int j = 0; j < KM; j++) wt[j] = w && j < k ? w[(int64_t)t * k + j] : 1.f;
         if (res.p) load8<DT>(res.p, (int64_t)t * res.ld + c, full ? 8 : H - c, res_f32, q);
@@ -134,14 +156,14 @@ k_combine(Mat o, const float *w, int T, int k, int H, Mat res, bool res_f32, Mat
 #pragma unroll
             for (int i = 0; i < 8; i++) acc[i] += q[i];
         }
-        put<DT, full>(y, t, c, H, y_f32, acc);
+        put<DT, full, PAST>(y, t, c, H, y_f32, acc);
     });
 }
 
 // One workgroup per token: d_o[t k + j] = w[t][j] dy[t] and, summed over the
 // row, dw[t][j] = <dy[t], o[t k + j]>: a thread's pieces in order, the lanes
 // by a tree, the waves in order.
-template <int DT, int KM>
+template <int DT, int KM, int PAST>
 __global__ void __launch_bounds__(256)
 k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int T, int k, int H, Mat d_o, float *dw) {
     __shared__ float part[KM][4];
@@ -159,7 +181,7 @@ k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int T, int k, int
         if (dw) {
 #pragma unroll
             for (int j = 0; j < KM; j++)
-                if (j < k) u[j] = piece<full>(o, (int64_t)t * k + j, c, H);
+                if (j < k) u[j] = piece<full, PAST>(o, (int64_t)t * k + j, c, H);
         }
         load8<DT>(dy.p, (int64_t)t * dy.ld + c, full ? 8 : H - c, dy_f32, d);
         if (d_o.p) {
@@ -170,7 +192,7 @@ k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int T, int k, int
                     float q[8];
 #pragma unroll
                     for (int i = 0; i < 8; i++) q[i] = wt[j] * d[i];
-                    put<DT, full>(d_o, (int64_t)t * k + j, c, H, false, q);
+                    put<DT, full, PAST>(d_o, (int64_t)t * k + j, c, H, false, q);
                 }
         }
         if (dw) {
@@ -216,13 +238,13 @@ k_act_backward(bm_host::ActBackward p, int rows_per, int want_sum) {
     auto at = [&](auto whole, int r) {
         constexpr bool full = decltype(whole)::value;
         float d[8], z[8];
-        const uint4 ud = piece<full>(dy, r, c, p.N), uz = p.pre ? piece<full>(pre, r, c, p.N) : make_uint4(0, 0, 0, 0);
+        const uint4 ud = piece<full, kCached>(dy, r, c, p.N), uz = p.pre ? piece<full, kCached>(pre, r, c, p.N) : make_uint4(0, 0, 0, 0);
         values<DT>(ud, d);
         if (p.pre) {
             values<DT>(uz, z);
             slope_row(d, z, p.act);
         }
-        if (p.dz) put<DT, full>(dz, r, c, p.N, false, d);
+        if (p.dz) put<DT, full, kCached>(dz, r, c, p.N, false, d);
 #pragma unroll
         for (int j = 0; j < 8; j++) sum[j] += d[j];
     };
@@ -274,28 +296,26 @@ k_bias_grad(const float *partial, int slices, int N, void *db, int db_dtype) {
 
 Mat mat(const bitmoe_rows *m) { return m ? Mat{m->data, m->ld} : Mat{nullptr, 0}; }
 
-template <int KM>
-int combine_k(const bitmoe_rows &o, const float *w, int T, int k, const bitmoe_rows *res, const bitmoe_rows &y,
-              hipStream_t s) {
-    const Grid2 g = pieces_grid(T, o.cols);
-    const bool rt = res && res->dtype == BITMOE_F32, yt = y.dtype == BITMOE_F32;
-    if (o.dtype == BITMOE_BF16)
-        k_combine<BITMOE_BF16, KM><<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(res), rt, mat(&y), yt, g.cshift);
-    else
-        k_combine<BITMOE_F16, KM><<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(res), rt, mat(&y), yt, g.cshift);
-    BM_LAUNCH_CHECK();
-    return BITMOE_OK;
+// f(type, past) with both as constants
+template <class F>
+int with(int dtype, int64_t bytes, F f) {
+    auto typed = [&](auto dt) {
+        switch (past_cache(bytes)) {
+            case kCached: return f(dt, std::integral_constant<int, kCached>{});
+            case kLoadsPast: return f(dt, std::integral_constant<int, kLoadsPast>{});
+            default: return f(dt, std::integral_constant<int, kAllPast>{});
+        }
+    };
+    return dtype == BITMOE_BF16 ? typed(std::integral_constant<int, BITMOE_BF16>{})
+                                : typed(std::integral_constant<int, BITMOE_F16>{});
 }
-template <int KM>
-int combine_backward_k(const bitmoe_rows &dy, const bitmoe_rows *o, const float *w, int T, int k,
-                       const bitmoe_rows *d_o, float *dw, int dtype, hipStream_t s) {
-    const int block = dy.cols <= 512 ? 64 : 256;
-    if (dtype == BITMOE_BF16)
-        k_combine_backward<BITMOE_BF16, KM><<<T, block, 0, s>>>(mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, T, k, dy.cols, mat(d_o), dw);
-    else
-        k_combine_backward<BITMOE_F16, KM><<<T, block, 0, s>>>(mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, T, k, dy.cols, mat(d_o), dw);
-    BM_LAUNCH_CHECK();
-    return BITMOE_OK;
+// f(at least k) as a constant
+template <class F>
+int with_k(int k, F f) {
+    if (k <= 2) return f(std::integral_constant<int, 2>{});
+    if (k <= 4) return f(std::integral_constant<int, 4>{});
+    if (k <= 8) return f(std::integral_constant<int, 8>{});
+    return f(std::integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -304,41 +324,50 @@ namespace bm_host {
 
 int launch_swiglu(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows &h, int dtype, hipStream_t s) {
     const Grid2 g = pieces_grid(gate.rows, gate.cols);
-    if (dtype == BITMOE_BF16)
-        k_swiglu<BITMOE_BF16><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), mat(&h), gate.rows, gate.cols, g.cshift);
-    else
-        k_swiglu<BITMOE_F16><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), mat(&h), gate.rows, gate.cols, g.cshift);
-    BM_LAUNCH_CHECK();
-    return BITMOE_OK;
+    return with(dtype, (int64_t)gate.rows * gate.cols * 6, [&](auto dt, auto past) {
+        k_swiglu<dt.value, past.value><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), mat(&h), gate.rows, gate.cols, g.cshift);
+        BM_LAUNCH_CHECK();
+        return BITMOE_OK;
+    });
 }
 
 int launch_swiglu_backward(const bitmoe_rows &dh, const bitmoe_rows &gate, const bitmoe_rows &up,
                            const bitmoe_rows &dgate, const bitmoe_rows &dup, int dtype, hipStream_t s) {
     const Grid2 g = pieces_grid(gate.rows, gate.cols);
-    if (dtype == BITMOE_BF16)
-        k_swiglu_backward<BITMOE_BF16><<<g.grid, 256, 0, s>>>(mat(&dh), mat(&gate), mat(&up), mat(&dgate), mat(&dup),
-                                                              gate.rows, gate.cols, g.cshift);
-    else
-        k_swiglu_backward<BITMOE_F16><<<g.grid, 256, 0, s>>>(mat(&dh), mat(&gate), mat(&up), mat(&dgate), mat(&dup),
-                                                             gate.rows, gate.cols, g.cshift);
-    BM_LAUNCH_CHECK();
-    return BITMOE_OK;
+    return with(dtype, (int64_t)gate.rows * gate.cols * 10, [&](auto dt, auto past) {
+        k_swiglu_backward<dt.value, past.value><<<g.grid, 256, 0, s>>>(mat(&dh), mat(&gate), mat(&up), mat(&dgate),
+                                                                       mat(&dup), gate.rows, gate.cols, g.cshift);
+        BM_LAUNCH_CHECK();
+        return BITMOE_OK;
+    });
 }
 
 int launch_combine(const bitmoe_rows &o, const float *w, int T, int k, const bitmoe_rows *residual,
                    const bitmoe_rows &y, hipStream_t s) {
-    if (k <= 2) return combine_k<2>(o, w, T, k, residual, y, s);
-    if (k <= 4) return combine_k<4>(o, w, T, k, residual, y, s);
-    if (k <= 8) return combine_k<8>(o, w, T, k, residual, y, s);
-    return combine_k<16>(o, w, T, k, residual, y, s);
+    const Grid2 g = pieces_grid(T, o.cols);
+    const bool rt = residual && residual->dtype == BITMOE_F32, yt = y.dtype == BITMOE_F32;
+    return with_k(k, [&](auto km) {
+        return with(o.dtype, (int64_t)T * o.cols * 2 * (k + 2), [&](auto dt, auto past) {
+            k_combine<dt.value, km.value, past.value>
+                <<<g.grid, 256, 0, s>>>(mat(&o), w, T, k, o.cols, mat(residual), rt, mat(&y), yt, g.cshift);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        });
+    });
 }
 
 int launch_combine_backward(const bitmoe_rows &dy, const bitmoe_rows *o, const float *w, int T, int k,
                             const bitmoe_rows *d_o, float *dw, int dtype, hipStream_t s) {
-    if (k <= 2) return combine_backward_k<2>(dy, o, w, T, k, d_o, dw, dtype, s);
-    if (k <= 4) return combine_backward_k<4>(dy, o, w, T, k, d_o, dw, dtype, s);
-    if (k <= 8) return combine_backward_k<8>(dy, o, w, T, k, d_o, dw, dtype, s);
-    return combine_backward_k<16>(dy, o, w, T, k, d_o, dw, dtype, s);
+    const int block = dy.cols <= 512 ? 64 : 256;
+    const int64_t bytes = (int64_t)T * dy.cols * 2 * (1 + k * ((dw != nullptr) + (d_o != nullptr)));
+    return with_k(k, [&](auto km) {
+        return with(dtype, bytes, [&](auto dt, auto past) {
+            k_combine_backward<dt.value, km.value, past.value>
+                <<<T, block, 0, s>>>(mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, T, k, dy.cols, mat(d_o), dw);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        });
+    });
 }
 
 // about 8 blocks a compute unit, at least 16 rows each
