@@ -74,7 +74,7 @@ GROUPS = {
 }
 # N, K, padding between rows, first element's place: rows on 16 bytes, odd sizes, odd strides, odd addresses
 SHAPES = [(128, 64, 0, 0), (256, 256, 0, 0), (1, 1, 0, 0), (17, 33, 0, 0), (200, 104, 8, 8), (96, 72, 3, 1),
-          (264, 520, 0, 0), (130, 7, 1, 0), (512, 1024, 0, 0)]
+          (264, 520, 0, 0), (130, 7, 1, 0), (512, 1024, 0, 0), (130, 72, 0, 0), (7, 1096, 0, 0), (1, 64, 0, 0)]
 
 
 def experts_case(groups, N, K, dtype, pad, shift, seed=0):
@@ -196,6 +196,151 @@ def test_maps_gather_and_scatter(bm, T, k, E, N, K):
     dw = bm.expert_matmul_dw(dy, x, off, dy_rows=bad.cuda(), x_rows=bad.cuda(), x_div=k)
     want, mag = ex.expert_dw(ex.mapped(dy64, bad), ex.mapped(x64, bad, k), off.cpu())
     check(dw, want, ex.half_ulp(BF) * want.abs() + ex.sum_bound(T) * mag, "dw, entries outside")
+
+
+def compare(got, want, bound, what):
+    """check() where the operands are large: the oracle's products in float64
+    on the GPU."""
+    assert torch.isfinite(got).all(), what
+    d = (got.double() - want).abs()
+    worst = (d / (bound + TINY)).max().item()
+    say(f"[experts] {what}: largest error {worst:.2f} of its bound")
+    assert worst <= 1, what
+
+
+def large(g, *shape, dtype=BF, scale=1.0):
+    return torch.empty(*shape, dtype=dtype, device="cuda").normal_(0, scale, generator=g)
+
+
+# (E, rows of the groups, N, K): more tiles than compute units, of every size and an uneven end; few tiles and a
+# long contraction, which is split
+MANY = [(1, [5000], 2840, 200), (3, [4100, 0, 2000], 1992, 328), (40, [150, 3, 90, 400] * 10, 1160, 456),
+        (300, [37] * 300, 392, 264), (1, [8192], 2816, 72)]
+SPLIT = [(1, [64], 128, 4096), (1, [300], 200, 7168), (4, [5, 0, 17, 2], 136, 4104), (1, [1], 8, 6144),
+         (2, [130, 257], 257, 2056)]
+
+
+@pytest.mark.parametrize("case", MANY + SPLIT, ids=lambda c: f"E{c[0]}R{sum(c[1])}N{c[2]}K{c[3]}")
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+def test_many_tiles_and_split_contractions(bm, case, dtype):
+    E, counts, N, K = case
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    off = offsets_of(counts)
+    R = int(off[-1])
+    if case in SPLIT:
+        assert bm.expert_matmul_workspace_bytes(bm.MATMUL, E, R, N, K) > 0
+    x, w, dy = large(g, R, K, dtype=dtype), large(g, E, N, K, dtype=dtype), large(g, R, N, dtype=dtype)
+    perm = torch.randperm(R, generator=gen(1)).to(torch.int32).cuda()
+    say(f"[experts] E={E} R={R} N={N} K={K} {dtype}")
+    offc = off.cuda()
+    y, y32 = bm.expert_matmul(x, w, offc, y_rows=perm), bm.expert_matmul(x, w, offc, x_rows=perm, out_dtype=F32)
+    dx = bm.expert_matmul_dx(dy, w, offc, dy_rows=perm)
+    dw = bm.expert_matmul_dw(dy, x, offc, dy_rows=perm)
+    dw2 = bm.expert_matmul_dw(dy, x, offc, out_dtype=F32)
+    for a, f in ((y, lambda: bm.expert_matmul(x, w, offc, y_rows=perm)),
+                 (dw, lambda: bm.expert_matmul_dw(dy, x, offc, dy_rows=perm))):
+        assert torch.equal(a, f())                                      # the same bits again
+    u, small = ex.half_ulp(dtype), 2.0 ** -24 * (dtype == HF)
+    p = perm.long()
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        wd, xs, dys = w[e].double(), x[s].double(), dy[p[s]].double()
+        want, mag = xs @ wd.t(), xs.abs() @ wd.abs().t()
+        if s.stop > s.start:
+            compare(y[p[s]], want, u * want.abs() + ex.sum_bound(K) * mag + small, f"y of expert {e}")
+            xg = x[p[s]].double()
+            want, mag = xg @ wd.t(), xg.abs() @ wd.abs().t()
+            compare(y32[s], want, 2.0 ** -24 * want.abs() + ex.sum_bound(K) * mag, f"y32 of expert {e}")
+            want, mag = dys @ wd, dys.abs() @ wd.abs()
+            compare(dx[s], want, u * want.abs() + ex.sum_bound(N) * mag + small, f"dx of expert {e}")
+        n = s.stop - s.start
+        want, mag = dys.t() @ xs, dys.t().abs() @ xs.abs()
+        compare(dw[e], want, u * want.abs() + ex.sum_bound(n) * mag + small, f"dw of expert {e}")
+        dys = dy[s].double()
+        want, mag = dys.t() @ xs, dys.t().abs() @ xs.abs()
+        compare(dw2[e], want, 2.0 ** -24 * want.abs() + ex.sum_bound(n) * mag, f"dw32 of expert {e}")
+
+
+@pytest.mark.parametrize("N,K,R", [(128, 128, 8192), (72, 264, 4000), (17, 33, 3000)])
+def test_weights_gradient_split_over_rows(bm, N, K, R):
+    g = torch.Generator(device="cuda").manual_seed(R)
+    assert bm.expert_matmul_workspace_bytes(bm.MATMUL_DW, 2, R, N, K) >= 8 * 2 * N * K
+    dy, x = large(g, R, N), large(g, R, K)
+    off = offsets_of([R - 700, 500])                                    # 200 rows behind the last group
+    dy[R - 200:] = float("nan")
+    x[R - 200:] = float("nan")
+    perm = torch.arange(R - 1, -1, -1, dtype=torch.int32)
+    acc = large(g, 2, N, K, dtype=F32)
+    a64 = acc.double()
+    dw = bm.expert_matmul_dw(dy, x, off.cuda())
+    bm.expert_matmul_dw(dy, x, off.cuda(), dw=acc, accumulate=True)
+    dwm = bm.expert_matmul_dw(dy, x.flip(0), off.cuda(), x_rows=perm.cuda())
+    for e, s in ((0, slice(0, R - 700)), (1, slice(R - 700, R - 200))):
+        want, mag = dy[s].double().t() @ x[s].double(), dy[s].double().abs().t() @ x[s].double().abs()
+        bound = ex.half_ulp(BF) * want.abs() + ex.sum_bound(R) * mag
+        compare(dw[e], want, bound, f"dw {e}")
+        compare(dwm[e], want, bound, f"dw {e}, mapped")
+        compare(acc[e], a64[e] + want, 2.0 ** -23 * ((a64[e] + want).abs() + a64[e].abs()) + ex.sum_bound(R) * mag,
+                f"dw {e}, accumulated")
+
+
+@pytest.mark.parametrize("mapped", [False, True], ids=["contiguous", "mapped"])
+def test_operands_beyond_4_gib(bm, mapped):
+    """Rows and outputs more than 2^32 bytes from their matrix's beginning."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    K, N, rows = 7168, 136, 330000                                      # x: 4.7 GB
+    x = torch.empty(rows, K, dtype=BF, device="cuda")
+    n = 300
+    at = torch.cat([torch.arange(5), torch.arange(rows - n + 5, rows)])
+    x[at.cuda()] = large(g, n, K)
+    w, dy = large(g, 2, N, K, scale=K ** -0.5), large(g, n, N)
+    xs = x[at.cuda()].double()
+    if mapped:
+        m = at.to(torch.int32).cuda()
+        off = offsets_of([100, 200]).cuda()
+        y = bm.expert_matmul(x, w, off, x_rows=m)
+        out = torch.zeros(rows, K, dtype=BF, device="cuda")
+        bm.expert_matmul_dx(dy, w, off, dx_rows=m, dx=out)
+        dx = out[at.cuda()]
+        dw = bm.expert_matmul_dw(dy, x, off, x_rows=m)
+        groups = [slice(0, 100), slice(100, 300)]
+    else:
+        # only the last rows are in groups
+        first = rows - n + 5
+        off = torch.tensor([first, first + 100, rows], dtype=torch.int32).cuda()
+        full = torch.zeros(rows, N, dtype=BF, device="cuda")
+        bm.expert_matmul(x, w, off, y=full)
+        assert (full[:first] == 0).all()
+        y = torch.cat([full[:5], full[first:]])
+        fdy = torch.zeros(rows, N, dtype=BF, device="cuda")
+        fdy[at.cuda()] = dy
+        dx = bm.expert_matmul_dx(fdy, w, off, dx=torch.zeros(rows, K, dtype=BF, device="cuda"))[at.cuda()]
+        dw = bm.expert_matmul_dw(fdy, x, off)
+        groups = [slice(5, 105), slice(105, 300)]
+    for e, s in enumerate(groups):
+        d, wd = dy[s].double(), w[e].double()
+        want, mag = xs[s] @ wd.t(), xs[s].abs() @ wd.abs().t()
+        compare(y[s], want, ex.half_ulp(BF) * want.abs() + ex.sum_bound(K) * mag, f"y {e}")
+        want, mag = d @ wd, d.abs() @ wd.abs()
+        compare(dx[s], want, ex.half_ulp(BF) * want.abs() + ex.sum_bound(N) * mag, f"dx {e}")
+        want, mag = d.t() @ xs[s], d.abs().t() @ xs[s].abs()
+        compare(dw[e], want, ex.half_ulp(BF) * want.abs() + ex.sum_bound(200) * mag, f"dw {e}")
+
+
+@pytest.mark.parametrize("T,N,K", [(2048, 1000, 4096), (300, 1001, 2056), (4096, 520, 264), (1024, 2048, 7168)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_large(bm, T, N, K, act):
+    """Whole tiles and their edges with every part of the epilogue."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, w = large(g, T, K), large(g, N, K, scale=K ** -0.5)
+    b, r = large(g, N), large(g, T, N)
+    y, pre = bm.linear(x, w, bias=b, act=act, residual=r, keep_pre=True)
+    z, mag = x.double() @ w.double().t() + b.double(), x.double().abs() @ w.double().abs().t() + b.double().abs()
+    zb = ex.sum_bound(K + 1) * mag
+    compare(pre, z, ex.half_ulp(BF) * z.abs() + zb, "pre")
+    want = ex.act(z, act) + r.double()
+    compare(y, want, ex.half_ulp(BF) * want.abs() + 1.13 * zb + 2.0 ** -18 * (z.abs() + 1) + 2.0 ** -23 * r.double().abs(),
+            "y")
 
 
 def test_offsets_are_kept_inside_the_call(bm):
