@@ -92,7 +92,8 @@ def _load(path: str) -> C.CDLL:
         raise ImportError(f"{path} is not built; run `python -m bit_moe_amd.build`")
     L = C.CDLL(path)
     P, I, I64, SZ = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
-    LP, RP, EP = C.POINTER(LayerStruct), C.POINTER(RowsStruct), C.POINTER(ExpertsStruct)
+    LP = C.POINTER(LayerStruct)
+    RP = EP = P            # bitmoe_rows and bitmoe_experts: a structure by reference, or its bytes
     sig = {
         "moe_route_workspace_bytes": ([LP, I, I], SZ),
         "moe_route": ([LP, P, I, I, P, P, P, P, SZ, P], I),
