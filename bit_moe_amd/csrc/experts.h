@@ -54,12 +54,13 @@ struct GemmArgs {
 
 // How a product runs: which kernel, its tiles, into how many parts the
 // contraction is split.  A rule on the sizes the host knows.
-enum GemmKind { kAny, kTile256, kTile128x256, kTile128, kTile64x128 };
+enum GemmKind { kAny, kTile256, kTile128x256, kTile128, kTile64x128, kFew };
 struct GemmPlan {
     int kind;
     int mt, nt;         // row tiles (of all groups, at most; kGradWeights: of an expert), column tiles
     int splits, kper;
     int64_t grid;       // workgroups that would take one tile each
+    int parts, chunks;  // kFew: its P and NC
     size_t ws;          // bytes: the parts' float32, then (kGradWeights) the rows of both maps
 };
 // every row begins on a 16-byte address and has whole 8-element pieces

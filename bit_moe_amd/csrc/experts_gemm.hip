@@ -26,12 +26,20 @@ k_join(GemmArgs g, const float *part, int rows, int cshift) {
         if (row < 0) continue;
         const float *p = part + (int64_t)r * g.N + n;
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int s = 0; s < g.splits; s++) {
-            float o[8];
-            load8<DT>(p, s * step, left, true, o);
+        // eight parts' loads together (one after another they took 9 us for 16)
+        for (int s0 = 0; s0 < g.splits; s0 += 8) {
+            float o[8][8];
+            if (left >= 8) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] += o[j];
+                for (int s = 0; s < 8; s++) load8<DT>(p, min(s0 + s, g.splits - 1) * step, 8, true, o[s]);
+            } else {
+                for (int s = 0; s < 8; s++) load8<DT>(p, min(s0 + s, g.splits - 1) * step, left, true, o[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < 8; s++)
+                if (s0 + s < g.splits)
+#pragma unroll
+                    for (int j = 0; j < 8; j++) v[j] += o[s][j];
         }
         if (left >= 8) {
             float bias[8], res[8];

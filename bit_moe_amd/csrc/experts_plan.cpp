@@ -17,10 +17,10 @@ struct Shape {
     double stage, fixed;        // us for 64 of the contraction with every compute unit at work, and per tile
 };
 const Shape kShapes[] = {
-    {kTile256, 256, 256, 1, 1.35, 8.0},
+    {kTile256, 256, 256, 1, 1.35, 9.5},
     {kTile128x256, 128, 256, 1, 0.80, 6.0},
-    {kTile128, 128, 128, 2, 0.90, 6.0},
-    {kTile64x128, 64, 128, 2, 0.60, 5.0},
+    {kTile128, 128, 128, 2, 0.90, 4.0},
+    {kTile64x128, 64, 128, 2, 0.60, 4.5},
 };
 
 void tiles(int layout, const GemmArgs &g, int bm, int bn, GemmPlan *p) {
@@ -60,9 +60,11 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
         for (int splits = 1; splits <= 16; splits *= 2) {
             if (splits > 1 && stages < 4 * splits) break;
             const double rounds = std::ceil(n * splits / (cus * s.slots));
-            // parts: written and read in fp32, and a launch
-            const double join = splits == 1 ? 0 : 4 + out * 4 * (splits + 1) / 4e6;
-            const double us = rounds * (std::ceil(stages / splits) * s.stage + s.fixed) + join;
+            // parts: written and read in fp32, and a launch with the wait for it
+            const double join = splits == 1 ? 0 : 7 + out * 4 * (splits + 1) / 4e6;
+            // (a stage takes about three quarters of its time where the GPU is nearly empty)
+            const double fill = std::min(1.0, n * splits / (cus * s.slots));
+            const double us = rounds * (std::ceil(stages / splits) * s.stage * (0.75 + 0.25 * fill) + s.fixed) + join;
             if (us < least) {
                 least = us;
                 best.kind = whole ? s.kind : kAny;
@@ -72,6 +74,23 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
                 best.ws = splits == 1 ? 0 : ((size_t)out * 4 * splits + 255) / 256 * 256;
             }
         }
+    }
+    if (layout == kForward) {
+        // few rows: bound by the weights, read once per pass of up to 16 rows /
+        // parts * chunks of a group, and by x, read by every workgroup (from
+        // L2); one launch
+        int parts = 1;
+        while (parts < 4 && groups * std::ceil(g.N * parts / 16.0) < 2 * cus) parts *= 2;
+        const int nb = 16 / parts, chunks = g.R <= nb ? 1 : 4, per = nb * chunks;
+        const double nt = std::ceil(g.N / (double)nb), passes = std::max(1.0, rows / per);
+        const double us = 4 + groups * nt * nb * g.K * 2 * passes / 4.5e6 + (double)g.R * g.K * 2 * nt / 8e6;
+        GemmPlan few{};
+        few.kind = kFew;
+        few.splits = 1;
+        few.parts = parts;
+        few.chunks = chunks;
+        tiles(layout, g, per, nb, &few);
+        if (us < least && few.grid < 1 << 24) best = few;          // (a launch holds less than 2^32 threads)
     }
     if (layout == kGradWeights) best.ws += 2 * (((size_t)g.R * 4 + 255) / 256 * 256);
     return best;

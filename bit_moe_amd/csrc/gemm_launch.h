@@ -5,6 +5,7 @@
 #include <atomic>
 
 #include "gemm_any.h"
+#include "gemm_few.h"
 #include "gemm_tile.h"
 
 namespace bm {
@@ -29,6 +30,12 @@ int launch_tile(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t s) {
     return BITMOE_OK;
 }
 
+template <int DT, int P>
+void launch_few(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t s) {
+    if (p.chunks == 1) k_gemm_few<DT, P, 1><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
+    else k_gemm_few<DT, P, 4><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
+}
+
 template <int LAY, int DT>
 int launch_layout_of(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t s) {
     if constexpr (LAY == kGradWeights) {
@@ -46,6 +53,16 @@ int launch_layout_of(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t 
         case bm_host::kTile64x128:
             if constexpr (LAY != kGradWeights) return launch_tile<LAY, DT, 64, 128, 2, 2>(g, p, s);
             return BITMOE_EINVAL;
+    }
+    if (p.grid * 256 >= (int64_t)1 << 32) return BITMOE_EUNSUPPORTED;
+    if constexpr (LAY == kForward) {
+        if (p.kind == bm_host::kFew) {
+            if (p.parts == 1) launch_few<DT, 1>(g, p, s);
+            else if (p.parts == 2) launch_few<DT, 2>(g, p, s);
+            else launch_few<DT, 4>(g, p, s);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        }
     }
     k_gemm<LAY, DT, 128, 128, 2, 2><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
     BM_LAUNCH_CHECK();

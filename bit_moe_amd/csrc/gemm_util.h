@@ -187,11 +187,13 @@ struct Tiles {
             if (e < g.E) mine += (max(group_start(g, e + 1) - group_start(g, e), 0) + BM - 1) / BM;
         }
         incl = mine;
+        if (g.E == 1) incl = __builtin_amdgcn_readfirstlane(mine);
+        else
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(incl, o, kWave);
-            if (lane >= o) incl += v;
-        }
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(incl, o, kWave);
+                if (lane >= o) incl += v;
+            }
         items = (int64_t)__builtin_amdgcn_readlane(incl, 63) * nt;
         per_xcd = (items + 7) / 8;
     }

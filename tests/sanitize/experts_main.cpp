@@ -24,9 +24,12 @@ int launch_gemm(int layout, int, const GemmArgs &g, void *, hipStream_t) {
     launches++;
     for (int whole = 0; whole < 2; whole++) {
         const GemmPlan p = gemm_plan(layout, g, whole);
-        const int bm = p.kind == kTile256 ? 256 : p.kind == kTile64x128 ? 64 : 128;
-        const int bn = p.kind == kTile256 || p.kind == kTile128x256 ? 256 : 128;
-        EXPECT(whole || p.kind == kAny);
+        const bool few = p.kind == kFew;
+        const int bm = few ? 16 / p.parts * p.chunks : p.kind == kTile256 ? 256 : p.kind == kTile64x128 ? 64 : 128;
+        const int bn = few ? 16 / p.parts : p.kind == kTile256 || p.kind == kTile128x256 ? 256 : 128;
+        EXPECT(whole || few || p.kind == kAny);
+        EXPECT(!few || (layout == kForward && p.splits == 1 && (p.chunks == 1 || p.chunks == 4) &&
+                        (p.parts == 1 || p.parts == 2 || p.parts == 4) && p.grid * 256 < (int64_t)1 << 32));
         EXPECT(layout != kGradWeights || p.kind == kAny || p.kind == kTile256 || p.kind == kTile128);
         EXPECT(p.splits >= 1 && (int64_t)p.nt * bn >= g.N && (int64_t)(p.nt - 1) * bn < g.N);
         const int64_t n = (int64_t)p.mt * p.nt * p.splits;

@@ -228,7 +228,7 @@ def test_many_tiles_and_split_contractions(bm, case, dtype):
     off = offsets_of(counts)
     R = int(off[-1])
     if case in SPLIT:
-        assert bm.expert_matmul_workspace_bytes(bm.MATMUL, E, R, N, K) > 0
+        assert bm.expert_matmul_workspace_bytes(bm.MATMUL_DX, E, R, K, N) > 0 or R < 65
     x, w, dy = large(g, R, K, dtype=dtype), large(g, E, N, K, dtype=dtype), large(g, R, N, dtype=dtype)
     perm = torch.randperm(R, generator=gen(1)).to(torch.int32).cuda()
     say(f"[experts] E={E} R={R} N={N} K={K} {dtype}")
