@@ -63,13 +63,15 @@ k_join(GemmArgs g, const float *part, int rows, int cshift) {
     }
 }
 
-// the rows that two operands' maps give
+// The rows that two operands' maps give the weights' gradient; one that either
+// lacks adds nothing, whatever the other holds (0 times an infinity would).
 __global__ void __launch_bounds__(256)
 k_rows(GemmRows a, GemmRows b, int R, int32_t *arows, int32_t *brows) {
     const int r = blockIdx.x * 256 + threadIdx.x;
     if (r >= R) return;
-    arows[r] = row_of(a, r);
-    brows[r] = row_of(b, r);
+    const int ra = row_of(a, r), rb = row_of(b, r);
+    arows[r] = rb < 0 ? -1 : ra;
+    brows[r] = ra < 0 ? -1 : rb;
 }
 
 template <int LAY>

@@ -165,9 +165,9 @@ k_combine(Mat o, const float *w, int T, int k, int H, Mat res, bool res_f32, Mat
 // by a tree, the waves in order.
 template <int DT, int KM, int PAST>
 __global__ void __launch_bounds__(256)
-k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int T, int k, int H, Mat d_o, float *dw) {
+k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int t0, int k, int H, Mat d_o, float *dw) {
     __shared__ float part[KM][4];
-    const int t = blockIdx.x, tid = threadIdx.x, nw = blockDim.x >> 6;
+    const int t = t0 + blockIdx.x, tid = threadIdx.x, nw = blockDim.x >> 6;
     float wt[KM], dot[KM];
 #pragma unroll
     for (int j = 0; j < KM; j++) {
@@ -362,9 +362,12 @@ int launch_combine_backward(const bitmoe_rows &dy, const bitmoe_rows *o, const f
     const int64_t bytes = (int64_t)T * dy.cols * 2 * (1 + k * ((dw != nullptr) + (d_o != nullptr)));
     return with_k(k, [&](auto km) {
         return with(dtype, bytes, [&](auto dt, auto past) {
-            k_combine_backward<dt.value, km.value, past.value>
-                <<<T, block, 0, s>>>(mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, T, k, dy.cols, mat(d_o), dw);
-            BM_LAUNCH_CHECK();
+            constexpr int most = 1 << 23;               // (a launch holds less than 2^32 threads)
+            for (int t0 = 0; t0 < T; t0 += most) {
+                k_combine_backward<dt.value, km.value, past.value><<<std::min(T - t0, most), block, 0, s>>>(
+                    mat(&dy), dy.dtype == BITMOE_F32, mat(o), w, t0, k, dy.cols, mat(d_o), dw);
+                BM_LAUNCH_CHECK();
+            }
             return BITMOE_OK;
         });
     });

@@ -64,7 +64,9 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
             if (AKC) {
                 va[i] = load_piece(arow[i], k0 + 8 * ac[i], kend);
             } else {
-                const int kr = k0 + ar[i], row = kr < kend ? row_of(g.a, t.r0 + kr) : -1;
+                // (a row that either operand lacks adds nothing, whatever the other holds)
+                const int kr = k0 + ar[i];
+                const int row = kr < kend && row_of(g.b, t.r0 + kr) >= 0 ? row_of(g.a, t.r0 + kr) : -1;
                 va[i] = load_piece(row >= 0 ? A + (int64_t)row * g.a.ld : nullptr, m0 + 8 * ac[i], g.M);
             }
         }
@@ -76,7 +78,8 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
                 const int kr = k0 + br[i];
                 vb[i] = load_piece(kr < kend ? B + (int64_t)kr * g.b.ld : nullptr, n0 + 8 * bc[i], g.N);
             } else {
-                const int kr = k0 + br[i], row = kr < kend ? row_of(g.b, t.r0 + kr) : -1;
+                const int kr = k0 + br[i];
+                const int row = kr < kend && row_of(g.a, t.r0 + kr) >= 0 ? row_of(g.b, t.r0 + kr) : -1;
                 vb[i] = load_piece(row >= 0 ? B + (int64_t)row * g.b.ld : nullptr, n0 + 8 * bc[i], g.N);
             }
         }

@@ -348,7 +348,9 @@ BM_DEV float act_slope(float z, int act) {
         case BITMOE_ACT_GELU:
             return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
         case BITMOE_ACT_GELU_TANH: {
-            // with p = 1 / (1 + e^-2u): p + 2 z p (1 - p) du/dz
+            // with p = 1 / (1 + e^-2u): p + 2 z p (1 - p) du/dz; p is 0 or 1 long
+            // before |z| = 16, and z^2 may not be infinite beside it
+            z = z > 16.f ? 16.f : z < -16.f ? -16.f : z;
             const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z), p = 1.f / (1.f + __expf(-2.f * u));
             return p + 2.f * z * p * (1.f - p) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
         }

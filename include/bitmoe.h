@@ -463,6 +463,10 @@ int moe_pack_mxfp4(const void *src, void *dst, int E, int N, int K, void *stream
  *    of the call belong to expert e.  Values are clamped to [0, R]; rows in no
  *    group (behind the last one) are neither read nor written.
  *  - Outputs must not overlap inputs, except where a call says so.
+ *  - A workspace is one call's until the call has run: calls that may run at
+ *    once, captured graphs among them, need one each.
+ *  - Values meet only their formula: a combine weight of 0 times an infinity or
+ *    NaN is NaN, and so is such a value of W times a row that reads as zeros.
  *  - Results do not depend on scheduling (no atomics; sums in a fixed order).
  * Errors of all calls: EINVAL (null or misaligned pointer, size < 1 where
  * one is needed, ld < cols, sizes or types of the operands that do not agree),
@@ -495,7 +499,9 @@ typedef struct bitmoe_experts {
  *  moe_expert_matmul     y[r] = W_e x[r]        (x: K columns, y: N)
  *  moe_expert_matmul_dx  dx[r] = W_e^T dy[r]    (dy: N columns, dx: K)
  *  moe_expert_matmul_dw  dW_e = sum over e's rows r of dy[r] x[r]^T (N x K; 0
- *     for an expert without rows), added to what dw holds if accumulate != 0
+ *     for an expert without rows), added to what dw holds if accumulate != 0; a
+ *     row that a map takes from either operand adds nothing, whatever the other
+ *     operand holds there
  * with e the expert whose group row r lies in.  y, dx and dw may be
  * BITMOE_F32.  R = 0 does nothing (moe_expert_matmul_dw: every dW_e is 0).
  * E <= 1024.  ws: moe_expert_matmul_workspace_bytes(op, E, R, N, K) bytes of

@@ -284,6 +284,28 @@ def test_weights_gradient_split_over_rows(bm, N, K, R):
                 f"dw {e}, accumulated")
 
 
+@pytest.mark.parametrize("N,K,pad", [(256, 512, 0), (72, 40, 0), (33, 17, 1)])
+@pytest.mark.parametrize("side", ["dy", "x"])
+def test_weights_gradient_leaves_out_what_a_map_takes(bm, N, K, pad, side):
+    """A row that one operand's map takes adds nothing, though the other
+    operand's row holds infinities and NaN."""
+    R = 300
+    g = gen(N + K)
+    dy, dy64 = rnd(g, R, N, pad=pad)
+    x, x64 = rnd(g, R, K, pad=pad)
+    gone = torch.randperm(R, generator=g)[:90]
+    gone = torch.cat([gone, torch.arange(128, 192)])                    # a whole stage of the contraction among them
+    rows = torch.arange(R, dtype=torch.int32)
+    rows[gone] = torch.where(gone % 2 == 0, -1, R + 5).to(torch.int32)
+    hidden, h64 = (x, x64) if side == "dy" else (dy, dy64)
+    hidden[gone.cuda()] = torch.tensor([float("nan"), float("inf")], dtype=BF, device="cuda")[(gone % 2).cuda()][:, None]
+    h64[gone] = 0
+    off = offsets_of([100, 0, 190])
+    dw = bm.expert_matmul_dw(dy, x, off.cuda(), **{side + "_rows": rows.cuda()})
+    want, mag = ex.expert_dw(dy64, x64, off)
+    check(dw, want, ex.half_ulp(BF) * want.abs() + ex.sum_bound(R) * mag, f"dw without {side}'s rows, N={N} K={K}")
+
+
 @pytest.mark.parametrize("mapped", [False, True], ids=["contiguous", "mapped"])
 def test_operands_beyond_4_gib(bm, mapped):
     """Rows and outputs more than 2^32 bytes from their matrix's beginning."""
@@ -444,6 +466,15 @@ def test_linear_backward(bm, act, shape):
         assert [t is not None for t in b] == need and torch.equal(b[i], want)
 
 
+def test_slopes_of_far_values(bm):
+    """Slopes where the exponentials and squares on their way overflow."""
+    pre = torch.tensor([[-3e38, -1e20, -1e13, -200.0, 200.0, 1e13, 1e20, 3e38]], dtype=BF, device="cuda")
+    one, x, w = torch.ones_like(pre), pre[:, :1], pre.new_zeros(8, 1)
+    for act in ("relu", "gelu", "gelu_tanh", "silu"):
+        _, _, db = bm.linear_backward(one, x, w, act=act, pre=pre, need_dx=False, need_dw=False, need_db=True)
+        assert db.tolist() == [0.0] * 4 + [1.0] * 4, act
+
+
 @pytest.mark.parametrize("R,I,pad,shift", [(1, 1, 0, 0), (8, 2048, 0, 0), (3, 7, 0, 0), (300, 100, 4, 2), (70000, 8, 0, 0),
                                            (2, 4100, 0, 1)])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
@@ -516,6 +547,17 @@ def test_combine(bm, T, k, H, pad, shift, dtype):
     o2 = o.clone()
     d2, w2 = bm.combine_backward(dy, o2, wd, d_o=o2)
     assert torch.equal(o2, do) and torch.equal(w2, dw)
+
+
+def test_combine_backward_of_the_most_tokens(bm):
+    """2^24 tokens: more threads than one launch holds."""
+    T, H = 2 ** 24, 520
+    dy = torch.ones(T, H, dtype=BF, device="cuda")
+    w = (torch.arange(T, device="cuda") % 251).float().view(T, 1)      # (below 256: exact in bfloat16)
+    do, dw = bm.combine_backward(dy, dy, w)
+    assert (dw == H).all()
+    for t in range(0, T, 2 ** 22):
+        assert (do[t:t + 2 ** 22] == w[t:t + 2 ** 22].to(BF)).all()
 
 
 def layer(bm, x, wgu, wd, ids, wt, res, E, k):
