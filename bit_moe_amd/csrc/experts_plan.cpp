@@ -1,4 +1,24 @@
 // Which kernel a 16-bit product takes.  Host code only.
+//
+// A cost in us for each kernel and each number of parts of the contraction,
+// from the sizes the host knows (the groups' own sizes are on the device: they
+// are taken as even); the least wins.  Measured in bfloat16, us:
+//  one group, N 2048, K 7168     256x256  128x256  128x128  64x128  few rows   parts
+//     1 row                         21.0     14.7     13.3    11.3       6.8   of the best 16
+//     16                            21.8     15.7     14.4    12.5      12.5   16
+//     64                            25.8     20.5     20.8    19.9      34.5   8 (calls, not GPU time, from here on)
+//     512                           41.1     32.8     31.6    31.6             4
+//     1024                          53.3     43.6     46.0    47.9             4
+//     2048                          71.0     65.3     71.1    75.9             2
+//     8192                           191      199      221     277             1
+//  32 groups of 1024, N 7168, K 2048 879     1014     1182    1543             1
+//  256 groups of 8, N 4096, K 7168           2408     2477    2421             1
+//  the same, 64 each                3288     2540     2731    3642             1
+//  a split: 2048 rows, 128x256: 82.6 whole, 65.3 in 2 parts, 80.0 in 4; weights'
+//   gradient of 2048 x 2048 over 8192 rows, 256x256: 155 whole, 75.5 in 4 parts
+//  rows not on 16 bytes (N 2048, K 7168, 8192 rows): forward 358 against 201,
+//   rows' gradient 380 and 217, weights' gradient 575 and 195; only k_gemm
+//   can take them
 #include <algorithm>
 #include <cmath>
 
@@ -76,21 +96,31 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
         }
     }
     if (layout == kForward) {
-        // few rows: bound by the weights, read once per pass of up to 16 rows /
-        // parts * chunks of a group, and by x, read by every workgroup (from
-        // L2); one launch
-        int parts = 1;
-        while (parts < 4 && groups * std::ceil(g.N * parts / 16.0) < 2 * cus) parts *= 2;
-        const int nb = 16 / parts, chunks = g.R <= nb ? 1 : 4, per = nb * chunks;
-        const double nt = std::ceil(g.N / (double)nb), passes = std::max(1.0, rows / per);
-        const double us = 4 + groups * nt * nb * g.K * 2 * passes / 4.5e6 + (double)g.R * g.K * 2 * nt / 8e6;
-        GemmPlan few{};
-        few.kind = kFew;
-        few.splits = 1;
-        few.parts = parts;
-        few.chunks = chunks;
-        tiles(layout, g, per, nb, &few);
-        if (us < least && few.grid < 1 << 24) best = few;          // (a launch holds less than 2^32 threads)
+        // Few rows: a workgroup reads nb rows of W at 24 bytes a ns and its rows
+        // of x, which are in L2, at 44.  The tiles' kernels cannot beat the
+        // weights' bytes either.  Over parts 1, 2, 4: one row of 2048 x 7168 10.4,
+        // 6.8, 6.8 us, 8 rows 12.6, 8.9, 12.4; one of 512 x 7168 10.2, 6.6, 4.7; one
+        // of 16384 x 4096 22.8, 22.1, 23.2, 4 rows 24.2, 26.5, 33.4 (tiles 27.0), 16
+        // rows 31.2, 45.8, 76.5 (tiles 27.5).  Groups of more than two rows, of
+        // unknown evenness, are the tiles': 8 of 256 experts of 2048 x 2048, one row
+        // each 17.4 (tiles 19.2), two 18.5 (19.1), four 28.1 (17.0).
+        least = std::max(least, 5 + (double)groups * g.N * g.K * 2 / 6e6 + (best.splits > 1 ? 7 : 0));
+        for (int parts = 1; parts <= 4 && (g.E == 1 || rows <= 2); parts *= 2) {
+            const int nb = 16 / parts, chunks = rows <= nb ? 1 : 4, per = nb * chunks;
+            const double passes = std::ceil(rows / per), x = std::min(rows, (double)per);
+            const double each = std::max(1.0, groups * std::ceil(g.N / (double)nb) * passes / cus);    // of a compute unit
+            const double us = 5 + each * g.K * 2 * (nb / 24e3 + x / 44e3);
+            GemmPlan few{};
+            few.kind = kFew;
+            few.splits = 1;
+            few.parts = parts;
+            few.chunks = chunks;
+            tiles(layout, g, per, nb, &few);
+            if (us < least && few.grid < 1 << 24) {                // (a launch holds less than 2^32 threads)
+                least = us;
+                best = few;
+            }
+        }
     }
     if (layout == kGradWeights) best.ws += 2 * (((size_t)g.R * 4 + 255) / 256 * 256);
     return best;

@@ -5,10 +5,16 @@
 // (RP = 16 / P).  An operand's 16 rows are NB rows of W in P parts of the
 // contraction, and the other's RP rows of x in the same P parts; of the 16 x 16
 // product the P blocks on the diagonal are sums of one part each, added at the
-// end.  P > 1 gives a small matrix more workgroups (2048 outputs of one row: 512
+// end.  P > 1 gives a small matrix more workgroups (512 outputs of one row: 128
 // of 4 outputs each).  The 4 waves take a quarter of each part; lane l reads 8
 // values at a time of its row, and the four lanes of a row 128 bytes in two
 // loads (both operands order the contraction alike, in whatever order).
+// Bound by the weights' bytes, the most a compute unit can have on their way:
+// one row of 2048 x 7168 in 6.8 us (29 MB at 4.3 TB/s, about 2 us of it a
+// launch; repeated, so out of the memory-side cache), of 16384 x 4096 in 22.1
+// (134 MB at 6.1 TB/s).  x comes from L2 once per workgroup, at less than twice
+// W's rate, which ends the kernel's use at about 16 rows.  Through LDS in the tiles' kernels the same row takes 11.3
+// us: the parts' second launch and half-empty tiles.
 #pragma once
 
 #include "gemm_util.h"
