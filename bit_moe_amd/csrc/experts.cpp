@@ -247,7 +247,9 @@ int moe_linear_backward(const bitmoe_rows *dy, const bitmoe_rows *x, const bitmo
     if ((rc = check_ws(ws, ws_bytes, b.bytes))) return rc;
     hipStream_t s = as_stream(stream);
     char *base = static_cast<char *>(ws);
-    // dz replaces dy, where there is an activation to differentiate
+    // dz, in the operands' type, replaces dy where there is an activation to
+    // differentiate (a launch of its own: made inside the products it would be
+    // computed again by every column's tiles, 28 times at K 7168)
     bitmoe_rows dz = *dy;
     const bool slope = act != BITMOE_ACT_NONE && (dx || dw);
     if (slope && T > 0) {

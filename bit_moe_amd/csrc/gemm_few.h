@@ -11,7 +11,7 @@
 // loads (both operands order the contraction alike, in whatever order).
 // Bound by the weights' bytes, the most a compute unit can have on their way:
 // one row of 2048 x 7168 in 6.8 us (29 MB at 4.3 TB/s, about 2 us of it a
-// launch; repeated, so out of the memory-side cache), of 16384 x 4096 in 22.1
+// launch; repeated, so out of the memory-side cache; 9.1 from HBM), of 16384 x 4096 in 22.1
 // (134 MB at 6.1 TB/s).  x comes from L2 once per workgroup, at less than twice
 // W's rate, which ends the kernel's use at about 16 rows.  Through LDS in the tiles' kernels the same row takes 11.3
 // us: the parts' second launch and half-empty tiles.

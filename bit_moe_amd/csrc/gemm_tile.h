@@ -17,6 +17,20 @@
 // about 16 cycles for each; rows of 128 bytes because L2 serves 64-byte pieces
 // at half the rate (a ring of 32-wide stages ran 8192^3 at 1172 TFLOP/s, 1822
 // with its loads left out).
+//
+// Bound by the matrix cores where K is long: 16384 x 4096 x 7168 in bfloat16
+// takes 672 us forward and as rows' gradient (1432 TFLOP/s), 694 as weights'
+// gradient; 8192^3 841, 768 and 788.  The matrix cores are busy 75% of the time
+// at about 1.65 GHz, the clock that their own power leaves.  Where K is short
+// the tile's ends show: a round of 256 x 256 tiles costs 9.5 us beside 1.35 us a
+// stage, of which the epilogue's way through LDS is the most.  A workgroup stays
+// for several tiles and sends the next one's first stages off before the
+// epilogue (32 experts' down projection 943 -> 865 us).  Not taken: waits that
+// leave the last tile's stores on their way over the next one's first stages
+// (weights' gradient 1240 -> 1377 us: registers spilled), a tile's second half
+// skipped where its rows end in the first (1308 -> 1279 TFLOP/s in 8192^3 for
+// nothing gained over experts), lines of later stages touched into L2 (1308 ->
+// 1169).
 #pragma once
 
 #include <type_traits>
