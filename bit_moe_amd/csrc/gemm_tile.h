@@ -23,7 +23,7 @@
 // gradient; 8192^3 841, 768 and 788.  The matrix cores are busy 75% of the time
 // at about 1.65 GHz, the clock that their own power leaves.  Where K is short
 // the tile's ends show: a round of 256 x 256 tiles costs 9.5 us beside 1.35 us a
-// stage, of which the epilogue's way through LDS is the most.  A workgroup stays
+// stage, most of it the epilogue's stores (an epilogue without LDS was no faster).  A workgroup stays
 // for several tiles and sends the next one's first stages off before the
 // epilogue (32 experts' down projection 943 -> 865 us).  Not taken: waits that
 // leave the last tile's stores on their way over the next one's first stages
