@@ -53,20 +53,25 @@ BM_DEV const uint16_t *wave_ptr(const uint16_t *p) {
 }
 // 16 (4) bytes per lane to LDS, lane l's at `lds` (one for the wave) + 16 l
 // (4 l).  In asm, because the compiler would wait for it before the next LDS
-// read, of whatever stage; phase_barrier() waits instead.
+// read, of whatever stage; phase_barrier() waits instead.  The wait states that
+// the compiler would keep are therefore kept here: one between the write of m0
+// and the load that reads it (s_nop 0), and five between a vector instruction's
+// write of a scalar register (a readlane of a spilled base) and a load at it.  A
+// scalar copy of the base needs none on either side, and is the one for m0 too.
 BM_DEV void dma16(const void *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                 "v"(src) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 ::"{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
 }
 // the same with a base of the wave's and 32-bit offsets (bytes) of the lanes':
 // no arithmetic per load
 BM_DEV void dma16_from(const void *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                 "v"(off), "s"(base) : "memory");
+    uint64_t from;
+    asm volatile("s_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+                 : "=&s"(from) : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
 }
 BM_DEV void dma4(const void *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                 "v"(src) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off"
+                 ::"{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
 }
 // all but this wave's last N loads have arrived, its LDS reads are done, and
 // so for every wave of the workgroup
