@@ -116,24 +116,28 @@ int expert_rows_product(const bitmoe_rows *a, const bitmoe_experts *w, const int
     return launch_gemm(layout, w->dtype, g, ws, as_stream(stream));
 }
 
-// db's partial sums and dz, in moe_linear_backward's workspace
+// dz (two parts of whole 16-byte pieces a row), db's partial sums and the
+// products' own, in moe_linear_backward's workspace, whatever the call wants
 struct BackwardWs {
     size_t dz, db, gemm, bytes;
 };
+int64_t part_cols(int N) { return (N + 7) / 8 * 8; }
 BackwardWs backward_ws(int T, int N, int K) {
     GemmArgs g{};
     g.E = 1;
     g.R = T;
     BackwardWs b{};
     b.dz = 0;
-    b.db = up256((size_t)T * N * 2);
+    b.db = up256((size_t)T * part_cols(N) * 2 * 2);
     b.gemm = b.db + up256((size_t)act_backward_slices(T, N) * N * 4);
-    g.N = K;
-    g.K = N;
-    size_t n = gemm_ws_bytes(kGradRows, g);
     g.M = N;
     g.N = K;
-    n = std::max(n, gemm_ws_bytes(kGradWeights, g));
+    g.K = N;
+    size_t n = 0;
+    for (int64_t low : {(int64_t)0, part_cols(N)}) {
+        g.a_low = low;
+        n = std::max(n, std::max(gemm_ws_bytes(kGradRows, g), gemm_ws_bytes(kGradWeights, g)));
+    }
     b.bytes = b.gemm + n;
     return b;
 }
@@ -232,6 +236,8 @@ int moe_linear_backward(const bitmoe_rows *dy, const bitmoe_rows *x, const bitmo
     int rc = check_experts(w, T);
     if (rc) return rc;
     const int N = w->N, K = w->K, dt = w->dtype;
+    const bool rounded = act & BITMOE_ACT_ROUND_DZ;
+    act &= ~BITMOE_ACT_ROUND_DZ;
     if (w->E != 1 || check_act(act) || !is16(dt)) return BITMOE_EINVAL;
     if ((rc = check_rows(dy, T, N, false)) || dy->dtype != dt) return BITMOE_EINVAL;
     if (act != BITMOE_ACT_NONE && ((rc = check_rows(pre, T, N, false)) || pre->dtype != dt)) return BITMOE_EINVAL;
@@ -247,26 +253,34 @@ int moe_linear_backward(const bitmoe_rows *dy, const bitmoe_rows *x, const bitmo
     if ((rc = check_ws(ws, ws_bytes, b.bytes))) return rc;
     hipStream_t s = as_stream(stream);
     char *base = static_cast<char *>(ws);
-    // dz, in the operands' type, replaces dy where there is an activation to
-    // differentiate (a launch of its own: made inside the products it would be
-    // computed again by every column's tiles, 28 times at K 7168)
+    // dz replaces dy where there is an activation to differentiate (a launch of
+    // its own: made inside the products it would be computed again by every
+    // column's tiles, 28 times at K 7168): in two parts of the operands' type,
+    // which double the products' time; in one where the caller takes that
+    // rounding, or where it is none (relu)
     bitmoe_rows dz = *dy;
     const bool slope = act != BITMOE_ACT_NONE && (dx || dw);
+    const int64_t low = slope && T > 0 && act != BITMOE_ACT_RELU && !rounded ? part_cols(N) : 0;
     if (slope && T > 0) {
         dz.data = base + b.dz;
-        dz.ld = N;
+        dz.ld = (low ? 2 : 1) * part_cols(N);
     }
     if (slope || db) {
         const ActBackward p{dy->data, act != BITMOE_ACT_NONE ? pre->data : nullptr, slope ? dz.data : nullptr,
-                            dy->ld, act != BITMOE_ACT_NONE ? pre->ld : 0, dz.ld, T, N, act, db,
+                            dy->ld, act != BITMOE_ACT_NONE ? pre->ld : 0, dz.ld, low, T, N, act, db,
                             db_dtype, reinterpret_cast<float *>(base + b.db)};
         if ((rc = launch_act_backward(p, dt, s))) return rc;
     }
-    if (dx && T > 0 &&
-        (rc = launch_gemm(kGradRows, dt, rows_product(&dz, w, nullptr, T, dx, true), base + b.gemm, s)))
-        return rc;
-    if (dw && (rc = launch_gemm(kGradWeights, dt, weights_product(&dz, x, nullptr, T, dw, 0), base + b.gemm, s)))
-        return rc;
+    if (dx && T > 0) {
+        GemmArgs g = rows_product(&dz, w, nullptr, T, dx, true);
+        g.a_low = low;
+        if ((rc = launch_gemm(kGradRows, dt, g, base + b.gemm, s))) return rc;
+    }
+    if (dw) {
+        GemmArgs g = weights_product(&dz, x, nullptr, T, dw, 0);
+        g.a_low = low;
+        if ((rc = launch_gemm(kGradWeights, dt, g, base + b.gemm, s))) return rc;
+    }
     return BITMOE_OK;
 }
 

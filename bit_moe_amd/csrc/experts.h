@@ -50,6 +50,9 @@ struct GemmArgs {
     int64_t c_split;
     // kGradWeights with maps: the rows they give, or -1, of each of the call's
     const int32_t *arows, *brows;
+    // A (not kForward, no map) as two 16-bit parts of a half of each value
+    // (split16): the second's elements `a_low` further than the first's; 0: one
+    int64_t a_low;
 };
 
 // How a product runs: which kernel, its tiles, into how many parts the
@@ -74,11 +77,12 @@ int launch_experts_dx(int dtype, const GemmArgs &g, const GemmPlan &p, hipStream
 int launch_experts_dw(int dtype, const GemmArgs &g, const GemmPlan &p, hipStream_t s);
 
 // dz = dy act'(pre) (dz may be NULL) and, with db, its column sums by slices
-// of rows (partial [slices][N])
+// of rows (partial [slices][N]); low: dz in two parts, the second's that many
+// elements further (0: rounded to one)
 struct ActBackward {
     const void *dy, *pre;
     void *dz;
-    int64_t ld_dy, ld_pre, ld_dz;
+    int64_t ld_dy, ld_pre, ld_dz, low;
     int32_t T, N, act;
     void *db;
     int32_t db_dtype;

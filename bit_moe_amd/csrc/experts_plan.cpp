@@ -76,6 +76,7 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
                                                  : groups * std::max(1.0, rows / s.bm + 0.5);
         const double n = mt * ((g.N + s.bn - 1) / s.bn);
         const double k = layout == kGradWeights ? rows : g.K, stages = std::ceil(k / 64);
+        const double parts = g.a_low ? 2 : 1;           // (A's two parts one after the other)
         const double out = (double)(layout == kGradWeights ? (double)g.E * g.M : g.R) * g.N;
         for (int splits = 1; splits <= 16; splits *= 2) {
             if (splits > 1 && stages < 4 * splits) break;
@@ -84,7 +85,7 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
             const double join = splits == 1 ? 0 : 7 + out * 4 * (splits + 1) / 4e6;
             // (a stage takes about three quarters of its time where the GPU is nearly empty)
             const double fill = std::min(1.0, n * splits / (cus * s.slots));
-            const double us = rounds * (std::ceil(stages / splits) * s.stage * (0.75 + 0.25 * fill) + s.fixed) + join;
+            const double us = rounds * (std::ceil(stages / splits) * parts * s.stage * (0.75 + 0.25 * fill) + s.fixed) + join;
             if (us < least) {
                 least = us;
                 best.kind = whole ? s.kind : kAny;

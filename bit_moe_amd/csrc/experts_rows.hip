@@ -231,9 +231,10 @@ k_combine_backward(Mat dy, bool dy_f32, Mat o, const float *w, int t0, int k, in
     }
 }
 
-// dz = dy act'(pre), rounded to the operands' type because the matrix cores take
-// no other (by up to 2^-8 of each value in bfloat16, as dy itself was), and
-// the slice's column sums of dz before that rounding:
+// dz = dy act'(pre) in the operands' type, because the matrix cores take no
+// other: in two parts (split16), or rounded to one where the caller wants the
+// products in half the time or where one holds it all (relu).  With it the
+// slice's column sums of dz itself:
 // 32 threads over 256 columns, 8 over the slice's rows.
 template <int DT>
 __global__ void __launch_bounds__(256)
@@ -242,6 +243,7 @@ k_act_backward(bm_host::ActBackward p, int rows_per, int want_sum) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 256 + tx * 8;
     const int r0 = blockIdx.y * rows_per, r1 = min(r0 + rows_per, p.T);
     const Mat dy{const_cast<void *>(p.dy), p.ld_dy}, pre{const_cast<void *>(p.pre), p.ld_pre}, dz{p.dz, p.ld_dz};
+    const Mat low_part{static_cast<uint16_t *>(p.dz) + p.low, p.ld_dz};
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     auto at = [&](auto whole, int r) {
         constexpr bool full = decltype(whole)::value;
@@ -252,7 +254,14 @@ k_act_backward(bm_host::ActBackward p, int rows_per, int want_sum) {
             values<DT>(uz, z);
             slope_row(d, z, p.act);
         }
-        if (p.dz) put<DT, full, kCached>(dz, r, c, p.N, false, d);
+        if (p.dz && p.low) {
+            float high[8], low[8];
+            split16<DT>(d, high, low);
+            put<DT, full, kCached>(dz, r, c, p.N, false, high);
+            put<DT, full, kCached>(low_part, r, c, p.N, false, low);
+        } else if (p.dz) {
+            put<DT, full, kCached>(dz, r, c, p.N, false, d);
+        }
 #pragma unroll
         for (int j = 0; j < 8; j++) sum[j] += d[j];
     };

@@ -41,6 +41,9 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     const uint16_t *A = static_cast<const uint16_t *>(g.a.p);
     const uint16_t *B = static_cast<const uint16_t *>(g.b.p);
     if (LAY != kGradWeights) B += (int64_t)t.e * g.b_stride;
+    // A in two parts: the low one first, its sums scaled before the high one's
+    const bool parts = LAY != kForward && g.a_low;
+    if (parts) A += g.a_low;
 
     // pieces along a row keep their row over the stages
     const uint16_t *arow[PA], *brow[PB];
@@ -94,28 +97,41 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     for (int i = 0; i < TM; i++)
 #pragma unroll
         for (int j = 0; j < TN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (k.beg < kend) load(k.beg);
-    for (int k0 = k.beg; k0 < kend; k0 += kBK) {
+    for (bool low = parts;; low = false) {
+        if (k.beg < kend) load(k.beg);
+        for (int k0 = k.beg; k0 < kend; k0 += kBK) {
 #pragma unroll
-        for (int i = 0; i < PA; i++) *reinterpret_cast<uint4 *>(sa + (tid + i * NT) * 8) = va[i];
+            for (int i = 0; i < PA; i++) *reinterpret_cast<uint4 *>(sa + (tid + i * NT) * 8) = va[i];
 #pragma unroll
-        for (int i = 0; i < PB; i++) *reinterpret_cast<uint4 *>(sb + (tid + i * NT) * 8) = vb[i];
-        __syncthreads();
-        if (k0 + kBK < kend) load(k0 + kBK);
+            for (int i = 0; i < PB; i++) *reinterpret_cast<uint4 *>(sb + (tid + i * NT) * 8) = vb[i];
+            __syncthreads();
+            if (k0 + kBK < kend) load(k0 + kBK);
 #pragma unroll
-        for (int kk = 0; kk < kBK; kk += 32) {
-            s16x8 fa[TM], fb[TN];
+            for (int kk = 0; kk < kBK; kk += 32) {
+                s16x8 fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i++) fa[i] = frag<AKC, BM>(sa, wm * (BM / WM) + 16 * i, kk, lane);
+                for (int i = 0; i < TM; i++) fa[i] = frag<AKC, BM>(sa, wm * (BM / WM) + 16 * i, kk, lane);
 #pragma unroll
-            for (int j = 0; j < TN; j++) fb[j] = frag<BKC, BN>(sb, wn * (BN / WN) + 16 * j, kk, lane);
-            // (B first: a lane then holds four consecutive columns of one row)
+                for (int j = 0; j < TN; j++) fb[j] = frag<BKC, BN>(sb, wn * (BN / WN) + 16 * j, kk, lane);
+                // (B first: a lane then holds four consecutive columns of one row)
 #pragma unroll
-            for (int i = 0; i < TM; i++)
+                for (int i = 0; i < TM; i++)
 #pragma unroll
-                for (int j = 0; j < TN; j++) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
+                    for (int j = 0; j < TN; j++) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        if (!parts) break;
+        const float scale = low ? 1.f / low_scale<DT>() : 2.f;
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) acc[i][j] *= scale;
+        if (!low) break;
+        A -= g.a_low;
+#pragma unroll
+        for (int i = 0; i < PA; i++)
+            if (arow[i]) arow[i] -= g.a_low;
     }
     __syncthreads();         // (srow, where the loop did not run)
     tile_epilogue<LAY, DT, BM, BN, 1>(g, acc, reinterpret_cast<float *>(lds), srow, t.e, k.split, n0, wm * (BM / WM),

@@ -10,7 +10,7 @@
 
 namespace bm {
 
-template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS = false>
+template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS = false, bool PARTS = false>
 int launch_tile(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t s) {
     constexpr int lds = TileLds<LAY, BM, BN, WM, WN, MAPS>::bytes;
     // LDS above 64 KiB must be opted into per kernel and device
@@ -18,14 +18,14 @@ int launch_tile(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t s) {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return BITMOE_EHIP;
     if (dev > 63 || !(opted.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (hipFuncSetAttribute(reinterpret_cast<const void *>(k_gemm_tile<LAY, DT, BM, BN, WM, WN, MAPS>),
+        if (hipFuncSetAttribute(reinterpret_cast<const void *>(k_gemm_tile<LAY, DT, BM, BN, WM, WN, MAPS, PARTS>),
                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
             return BITMOE_EHIP;
         if (dev <= 63) opted.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
     }
     // as many workgroups as fit the GPU together, each for several tiles
     const int64_t most = std::max<int64_t>((int64_t)bm_host::cu_count() * (160 * 1024 / lds) / 8 * 8, 8);
-    k_gemm_tile<LAY, DT, BM, BN, WM, WN, MAPS><<<(int)std::min<int64_t>(p.grid, most), 64 * WM * WN, lds, s>>>(g, p.mt, p.nt);
+    k_gemm_tile<LAY, DT, BM, BN, WM, WN, MAPS, PARTS><<<(int)std::min<int64_t>(p.grid, most), 64 * WM * WN, lds, s>>>(g, p.mt, p.nt);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }
@@ -42,6 +42,18 @@ int launch_layout_of(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t 
         if (g.arows) switch (p.kind) {
             case bm_host::kTile256: return launch_tile<LAY, DT, 256, 256, 2, 4, true>(g, p, s);
             case bm_host::kTile128: return launch_tile<LAY, DT, 128, 128, 2, 2, true>(g, p, s);
+        }
+    }
+    if constexpr (LAY != kForward) {
+        if (g.a_low) switch (p.kind) {
+            case bm_host::kTile256: return launch_tile<LAY, DT, 256, 256, 2, 4, false, true>(g, p, s);
+            case bm_host::kTile128: return launch_tile<LAY, DT, 128, 128, 2, 2, false, true>(g, p, s);
+            case bm_host::kTile128x256:
+                if constexpr (LAY == kGradRows) return launch_tile<LAY, DT, 128, 256, 2, 4, false, true>(g, p, s);
+                return BITMOE_EINVAL;
+            case bm_host::kTile64x128:
+                if constexpr (LAY == kGradRows) return launch_tile<LAY, DT, 64, 128, 2, 2, false, true>(g, p, s);
+                return BITMOE_EINVAL;
         }
     }
     switch (p.kind) {

@@ -125,15 +125,17 @@ BM_DEV s16x8 frag_at(uint32_t at, int i, int kk) {
 }
 
 // MAPS (weights' gradient): the operands' rows are g.arows and g.brows (span32
-// is then of the whole operands).
-template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS>
+// is then of the whole operands).  PARTS (gradients): A is in two parts
+// (g.a_low); a tile takes all its stages over the low one, then, its sums scaled,
+// over the high one.
+template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS, bool PARTS>
 __global__ void __launch_bounds__(64 * WM * WN)
 k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     constexpr int NW = WM * WN, UM = BM / 2, UN = BN / 2;                  // a unit's rows
     constexpr int PA = UM * kBK / 8 / (64 * NW), PB = UN * kBK / 8 / (64 * NW);   // a unit's loads per wave
     constexpr int TI = UM / WM / 16, TJ = UN / WN / 16;                    // 16 x 16 products of a wave in a quadrant
     constexpr bool AKC = LAY != kGradWeights, BKC = LAY == kForward;
-    static_assert(LAY == kGradWeights || !MAPS, "");
+    static_assert((LAY == kGradWeights || !MAPS) && (LAY == kForward || MAPS ? !PARTS : true), "");
     constexpr int kUA = UM * kBK, kUB = UN * kBK, kStage = 2 * (kUA + kUB);       // elements
     static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW, "");
     extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
@@ -175,7 +177,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         whole = (kend - kbeg) / kBK;
         afast = g.a.span32;
         bfast = g.b.span32;
-        A = static_cast<const uint16_t *>(g.a.p);
+        A = static_cast<const uint16_t *>(g.a.p) + (PARTS ? g.a_low : 0);
         B = static_cast<const uint16_t *>(g.b.p);
         if (LAY != kGradWeights) B += (int64_t)t.e * g.b_stride;
         abase = A;
@@ -377,11 +379,14 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     enter(0);
     __syncthreads();           // xrow
     begin();
-    for (int par = 0;; par ^= 1) {
+    bool low = PARTS;          // A's low part is being multiplied
+    for (int par = 0;;) {
+        if (low == PARTS) {
 #pragma unroll
-        for (int i = 0; i < 2 * TI; i++)
+            for (int i = 0; i < 2 * TI; i++)
 #pragma unroll
-            for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
         if (stages > 0) {
             phase_barrier<3 * PA + 3 * PB + 2 * MAPS>();
 #pragma unroll
@@ -402,17 +407,34 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             }
         }
         // every wave is done with the stages, and the loads past the last
-        // stage have arrived: the next tile's may begin
+        // stage have arrived: the next tile's, or part's, may begin
         phase_barrier<0>();
+        const bool again = PARTS && low;
         const int e = t.e, n = n0, part = split;
-        const bool more = next();
-        if (more) enter(par ^ 1);
-        __syncthreads();       // xrow; srow, where no stage was
+        bool more = again;
+        if (again) {
+            A -= g.a_low;
+            abase -= g.a_low;
+        } else {
+            more = next();
+            if (more) enter(par ^ 1);
+            __syncthreads();       // xrow; srow, where no stage was
+        }
         if (more) begin();
+        if (PARTS) {
+            const float scale = again ? 1.f / low_scale<DT>() : 2.f;
+#pragma unroll
+            for (int i = 0; i < 2 * TI; i++)
+#pragma unroll
+                for (int j = 0; j < 2 * TJ; j++) acc[i][j] *= scale;
+        }
+        low = PARTS && !again;
+        if (again) continue;
         tile_epilogue<LAY, DT, BM, BN, 2>(
             g, acc, reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::out),
             srow + par * BM, e, part, n, wm * (UM / WM), wn * (UN / WN), wave, lane);
         if (!more) return;
+        par ^= 1;
     }
 }
 

@@ -44,6 +44,27 @@ BM_DEV uint32_t elem_pair(float a, float b) {
     else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2_t));
 }
 
+// A value in fp32 as two 16-bit ones for the matrix cores, which take no more:
+// a half of it rounded, and what that leaves, 2^8 (bfloat16) or 2^11 (float16)
+// times, so that v = 2 (high + low / low_scale).  What both leave is at most
+// 2^-16 (2^-22) of v or, in float16, 2^-35; the half keeps float16's largest
+// values from its infinity, and the low part's scale its smallest from zero.
+template <int DT>
+constexpr float low_scale() { return DT == BITMOE_BF16 ? 256.f : 2048.f; }
+template <int DT>
+BM_DEV void split16(const float (&v)[8], float (&high)[8], float (&low)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const uint32_t h = elem_pair<DT>(0.5f * v[j], 0.5f * v[j + 1]);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            high[j + i] = elem_f32<DT>(h >> (16 * i) & 0xFFFFu);
+            const float left = 0.5f * v[j + i] - high[j + i];
+            low[j + i] = fabsf(high[j + i]) < INFINITY ? left * low_scale<DT>() : 0.f;
+        }
+    }
+}
+
 // 16 bytes at any element's address: gfx950 reads and writes global
 // memory at any alignment, so rows need not be aligned to a vector
 struct __attribute__((packed, aligned(2))) U128 { uint32_t w[4]; };

@@ -16,6 +16,7 @@ import struct
 from ._lib import BF16, F16, F32, _check, _torch, lib
 
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+ROUND_DZ = 256          # or'ed to linear_backward's act
 MATMUL, MATMUL_DX, MATMUL_DW = 0, 1, 2
 
 # bitmoe_rows and bitmoe_experts as bytes: a call's operands are packed in a
@@ -282,11 +283,13 @@ def linear(x, w, bias=None, act="none", residual=None, keep_pre=False, y=None, p
 
 
 def linear_backward(dy, x, w, act="none", pre=None, dx=None, dw=None, db=None, need_dx=True, need_dw=True,
-                    need_db=False, out_dtype=None, ws=None, stream=None):
+                    need_db=False, out_dtype=None, ws=None, stream=None, round_dz=False):
     """Gradients of linear: with dz = dy act'(pre), (dx, dw, db) = (dz w,
     dz^T x, column sums of dz), None for what is not needed (given outputs are
     needed); new ones in out_dtype (default x's).  The residual's gradient is
-    dy."""
+    dy.  round_dz: dz is rounded to x's type before the products, which then
+    take half their time (else it enters them as two such values; db sums dz
+    itself either way)."""
     code = _act(act)
     if code and pre is None:
         raise ValueError("pre is needed with an activation")
@@ -294,7 +297,8 @@ def linear_backward(dy, x, w, act="none", pre=None, dx=None, dw=None, db=None, n
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
-            return linear_backward(dy, x, w, act, pre, dx, dw, db, need_dx, need_dw, need_db, out_dtype, ws)
+            return linear_backward(dy, x, w, act, pre, dx, dw, db, need_dx, need_dw, need_db, out_dtype, ws,
+                                   round_dz=round_dz)
     if len(w.shape) != 2:
         raise ValueError("w must have 2 dimensions")
     we = _experts(w, "w")
@@ -313,8 +317,8 @@ def linear_backward(dy, x, w, act="none", pre=None, dx=None, dw=None, db=None, n
     dbp, dbt = (None, F32) if db is None else (_vector(db, N, "db"), _dtype(db, "db", True))
     L = lib()
     hold, p, n = _scratch(ws, L.moe_linear_backward_workspace_bytes(T, N, K), dev)
-    _check(L.moe_linear_backward(dyr, xr, we, code, pr, dxr, dwe, dbp, dbt, p, n, _current_stream(dev)),
-           "moe_linear_backward")
+    _check(L.moe_linear_backward(dyr, xr, we, code | (ROUND_DZ if round_dz else 0), pr, dxr, dwe, dbp, dbt, p, n,
+                                 _current_stream(dev)), "moe_linear_backward")
     return dx, dw, db
 
 

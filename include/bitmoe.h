@@ -477,6 +477,7 @@ int moe_pack_mxfp4(const void *src, void *dst, int E, int N, int K, void *stream
 #define BITMOE_ACT_GELU      2   /* z/2 (1 + erf(z / sqrt 2)) */
 #define BITMOE_ACT_GELU_TANH 3   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
 #define BITMOE_ACT_SILU      4   /* z / (1 + e^-z) */
+#define BITMOE_ACT_ROUND_DZ  256 /* or'ed to act, moe_linear_backward only */
 
 typedef struct bitmoe_rows {
     void *data;            /* row i, column c at element i * ld + c */
@@ -530,10 +531,14 @@ int moe_expert_matmul_dw(const bitmoe_rows *dy, const bitmoe_rows *x, const int3
  * Backward, given dy [T][N] of x's type and (act != BITMOE_ACT_NONE) pre:
  *     dz = dy act'(pre);  dx = dz W;  dW = dz^T x;  db = column sums of dz
  * each written if its pointer is not NULL (dx, dw of x's type or BITMOE_F32,
- * db [N] of db_dtype); the residual's gradient is dy.  dz enters the products
- * rounded to x's type, and db before that rounding.  ReLU has slope 0 at 0.
+ * db [N] of db_dtype); the residual's gradient is dy.  dz enters the products as
+ * the sum of two values of x's type, within 2^-16 (bfloat16) or 2^-22 (float16;
+ * 2^-35 near 0) of it, which takes the products twice their time; with
+ * act | BITMOE_ACT_ROUND_DZ it is rounded to one (in float16 values from 65520
+ * become infinite, below 2^-25 zero).  db sums dz itself.  ReLU has slope 0 at 0.
  * ws: moe_linear_workspace_bytes(T, N, K), moe_linear_backward_workspace_bytes
- * (T, N, K) bytes, 256-byte aligned.  T = 0 does nothing (dw and db are 0).
+ * (T, N, K) bytes, 256-byte aligned (the backward's for any act and any of its
+ * outputs).  T = 0 does nothing (dw and db are 0).
  */
 size_t moe_linear_workspace_bytes(int T, int N, int K);
 int moe_linear(const bitmoe_rows *x, const bitmoe_experts *w, const void *bias, int act,

@@ -1,0 +1,49 @@
+"""What the 16-bit expert layer's calls accept, without a GPU: a call that
+passes every check asks for its workspace (BITMOE_EWORKSPACE) or, with no rows,
+queues nothing."""
+import ctypes as C
+import os
+import re
+
+import pytest
+
+import bit_moe_amd as bm
+from bit_moe_amd import experts as ex
+from bit_moe_amd._lib import BF16, EINVAL, EWORKSPACE, F16, F32, ExpertsStruct, RowsStruct
+
+P = 4096            # an aligned address that nothing dereferences
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "bitmoe.h")
+
+
+def rows(n=8, cols=16, data=P, map=None, ld=None, div=1, dtype=BF16):
+    return C.byref(RowsStruct(data, map, cols if ld is None else ld, n, cols, div, dtype))
+
+
+def experts(E=4, N=32, K=16, data=P, ld=None, stride=None, dtype=BF16):
+    ld = K if ld is None else ld
+    return C.byref(ExpertsStruct(data, ld, N * ld if stride is None else stride, E, N, K, dtype))
+
+
+def test_the_bindings_acts_are_the_headers():
+    src = open(HEADER).read()
+    names = {m[0].lower(): int(m[1]) for m in re.findall(r"#define BITMOE_ACT_(\w+)\s+(\d+)", src)}
+    assert names.pop("round_dz") == ex.ROUND_DZ
+    assert names == ex.ACTS
+
+
+@pytest.mark.parametrize("act", range(5))
+def test_backward_with_and_without_rounded_dz(act):
+    L = bm.lib()
+
+    def back(act, ws=None, n=0, dtype=BF16):
+        r = lambda cols: rows(cols=cols, dtype=dtype)  # noqa: E731
+        return L.moe_linear_backward(r(32), r(16), experts(E=1, dtype=dtype), act, r(32), r(16), experts(E=1, dtype=dtype),
+                                     P, F32, ws, n, None)
+    need = L.moe_linear_backward_workspace_bytes(8, 32, 16)
+    assert need >= 8 * 32 * 2 * 2                        # dz in two parts
+    for dtype in (BF16, F16):
+        assert back(act, dtype=dtype) == back(act | ex.ROUND_DZ, dtype=dtype) == EWORKSPACE
+        assert back(act | ex.ROUND_DZ, P, need - 1, dtype) == EWORKSPACE
+    assert back(act | 512) == EINVAL and back(5 | ex.ROUND_DZ) == EINVAL
+    # the forward pass knows no such flag
+    assert L.moe_linear(rows(n=0), experts(E=1), None, act | ex.ROUND_DZ, None, None, rows(n=0, cols=32), None, 0, None) == EINVAL
