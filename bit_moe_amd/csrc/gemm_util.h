@@ -337,7 +337,9 @@ BM_DEV s16x8 frag(const uint16_t *tile, int x0, int kk, int lane) {
 BM_DEV float act_fwd(float z, int act) {
     switch (act) {
         case BITMOE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-        case BITMOE_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+        // (1 + erf of a negative number is erfc of the positive one, which keeps the
+        // digits that the sum cancels: all of them below z = -5.5)
+        case BITMOE_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);
         case BITMOE_ACT_GELU_TANH: {
             // 0.5 (1 + tanh u) = 1 / (1 + e^-2u)
             const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
@@ -367,7 +369,7 @@ BM_DEV float act_slope(float z, int act) {
     switch (act) {
         case BITMOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
         case BITMOE_ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+            return 0.5f * erfcf(z * -0.70710678118654752f) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
         case BITMOE_ACT_GELU_TANH: {
             // with p = 1 / (1 + e^-2u): p + 2 z p (1 - p) du/dz; p is 0 or 1 long
             // before |z| = 16, and z^2 may not be infinite beside it

@@ -153,3 +153,31 @@ def test_linear_backward_of_rounded_dz(bm, act, shape):
         for got, want, err, mag in ((dx, dz @ w, e @ w.abs(), m @ w.abs()),
                                     (dw, dz.t() @ x, e.t() @ x.abs(), m.t() @ x.abs())):
             assert over(got, want, err + ex.sum_bound(4) * mag + 2.0 ** -24 * want.abs()) <= 1
+
+
+@pytest.mark.parametrize("T,K", [(1, 1), (40, 40), (300, 64), (1500, 1032)])
+def test_gelu_of_negative_values(bm, T, K):
+    """Relative to the value, down to where float32 ends: a sum of 1 and erf
+    would leave nothing of it."""
+    z = torch.arange(-13.0, -2.0, 1 / 64).to(HF)                                # (exact in float16)
+    x, w = torch.zeros(T, K, dtype=HF), torch.zeros(z.numel(), K, dtype=HF)
+    x[:, 0], w[:, 0] = 1, z
+    z64 = z.double()
+    # The argument z / sqrt 2 is off by 2^-23 of itself, twice its square, 169, times that in the result: 2^-15.6;
+    # erfc's own error and the products' roundings, together below 2^-18.  A value below 2^-126 may be lost.
+    y, _ = bm.linear(x.cuda(), w.cuda(), act="gelu", out_dtype=F32)
+    want = ex.act(z64, "gelu").cuda()
+    assert (want[-1] < -0.01) and (want < 0).all()
+    worst = over(y, want, 2.0 ** -15.3 * want.abs() + 2.0 ** -126)
+    say(f"[experts] gelu T={T}: largest error {worst:.2f} of its bound")
+    assert worst <= 1
+    # The slope's two terms, of opposite signs, the first at most a quarter of the second: 2^-15.6 / 4 of the first,
+    # and of the second e^(-z^2 / 2) with an argument to 85, off by 2^-23 of itself in the square and again in the
+    # exponential's base 2: 2^-15.6; both over the three quarters that are left.
+    if T == 1:
+        _, _, db = bm.linear_backward(torch.ones(1, z.numel(), dtype=HF, device="cuda"), x.cuda(), w.cuda(), act="gelu",
+                                      pre=z.cuda()[None], need_dx=False, need_dw=False, need_db=True, out_dtype=F32)
+        want = ex.act_slope(z64, "gelu").cuda()
+        worst = over(db, want, 2.0 ** -14.8 * want.abs() + 2.0 ** -124)
+        say(f"[experts] gelu's slope: largest error {worst:.2f} of its bound")
+        assert worst <= 1
