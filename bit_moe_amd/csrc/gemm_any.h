@@ -18,7 +18,10 @@ BM_DEV uint4 load_piece(const uint16_t *row, int c8, int end) {
     return load16_part(row + c8, end - c8);
 }
 
-template <int LAY, int DT, int BM, int BN, int WM, int WN>
+// PARTS (gradients): A is in two parts (g.a_low); the low one first, its sums
+// scaled before the high one's.  (An instance of its own: in one for both the
+// weights' gradient took 260 registers, which is one workgroup a unit, not two.)
+template <int LAY, int DT, int BM, int BN, int WM, int WN, bool PARTS>
 __global__ void __launch_bounds__(64 * WM * WN)
 k_gemm(GemmArgs g, int mtiles, int ntiles) {
     constexpr int NT = 64 * WM * WN, PA = BM * kBK / 8 / NT, PB = BN * kBK / 8 / NT;
@@ -41,9 +44,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     const uint16_t *A = static_cast<const uint16_t *>(g.a.p);
     const uint16_t *B = static_cast<const uint16_t *>(g.b.p);
     if (LAY != kGradWeights) B += (int64_t)t.e * g.b_stride;
-    // A in two parts: the low one first, its sums scaled before the high one's
-    const bool parts = LAY != kForward && g.a_low;
-    if (parts) A += g.a_low;
+    if (PARTS) A += g.a_low;
 
     // pieces along a row keep their row over the stages
     const uint16_t *arow[PA], *brow[PB];
@@ -97,7 +98,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
     for (int i = 0; i < TM; i++)
 #pragma unroll
         for (int j = 0; j < TN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (bool low = parts;; low = false) {
+    for (bool low = PARTS;; low = false) {
         if (k.beg < kend) load(k.beg);
         for (int k0 = k.beg; k0 < kend; k0 += kBK) {
 #pragma unroll
@@ -121,7 +122,7 @@ k_gemm(GemmArgs g, int mtiles, int ntiles) {
             }
             __syncthreads();
         }
-        if (!parts) break;
+        if (!PARTS) break;
         const float scale = low ? 1.f / low_scale<DT>() : 2.f;
 #pragma unroll
         for (int i = 0; i < TM; i++)

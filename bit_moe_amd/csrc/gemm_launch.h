@@ -76,7 +76,14 @@ int launch_layout_of(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t 
             return BITMOE_OK;
         }
     }
-    k_gemm<LAY, DT, 128, 128, 2, 2><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
+    if constexpr (LAY != kForward) {
+        if (g.a_low) {
+            k_gemm<LAY, DT, 128, 128, 2, 2, true><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        }
+    }
+    k_gemm<LAY, DT, 128, 128, 2, 2, false><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }
