@@ -16,11 +16,16 @@
 //  the same, 64 each                3288     2540     2731    3642             1
 //  a split: 2048 rows, 128x256: 82.6 whole, 65.3 in 2 parts, 80.0 in 4; weights'
 //   gradient of 2048 x 2048 over 8192 rows, 256x256: 155 whole, 75.5 in 4 parts
-//  rows not on 16 bytes (N 2048, K 7168, 8192 rows): forward 358 against 201,
-//   rows' gradient 380 and 217, weights' gradient 575 and 195; only k_gemm
-//   can take them
+//  rows not on 16 bytes, which only k_gemm and the few-rows kernel can take
+//   (8192 rows): N 2048, K 7168 one element off, forward 358 against 201, rows'
+//   gradient 380 and 217, weights' gradient 575 and 195; N 2049, K 7167 in parts
+//   1, 2, 4, 8, 16: forward 453 511 578, rows' gradient 474 719, weights'
+//   gradient 1314 1104 990 1020 1193; 16 rows forward 119 68 41 28 24 (few rows
+//   48), rows' gradient 136 78 50 35; weights' gradient of 4097 x 1023 over 16384
+//   rows 2020 1235 800 644 651
 #include <algorithm>
 #include <cmath>
+#include <iterator>
 
 #include "experts.h"
 
@@ -41,6 +46,12 @@ const Shape kShapes[] = {
     {kTile128x256, 128, 256, 1, 0.80, 6.0},
     {kTile128, 128, 128, 2, 0.90, 4.0},
     {kTile64x128, 64, 128, 2, 0.60, 4.5},
+};
+// by layout: its loads wait for one another where rows run along the tile
+const Shape kAnyShapes[] = {
+    {kAny, 128, 128, 2, 1.15, 5.0},
+    {kAny, 128, 128, 2, 3.60, 4.0},
+    {kAny, 128, 128, 2, 4.50, 4.0},
 };
 
 void tiles(int layout, const GemmArgs &g, int bm, int bn, GemmPlan *p) {
@@ -68,8 +79,11 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
     const double cus = cu_count();
     const int groups = std::min(g.E, std::max(g.R, 1));
     const double rows = (double)g.R / groups;             // of a group
-    for (const Shape &s : kShapes) {
-        if (whole ? layout == kGradWeights && s.bm != s.bn : s.kind != kTile128) continue;
+    const Shape *const first = whole ? kShapes : kAnyShapes + layout;
+    const Shape *const last = whole ? std::end(kShapes) : first + 1;
+    for (const Shape *at = first; at < last; at++) {
+        const Shape &s = *at;
+        if (layout == kGradWeights && s.bm != s.bn) continue;
         // tiles expected: a group's last row tile is half full on average
         const double mt = layout == kGradWeights ? (double)groups * ((g.M + s.bm - 1) / s.bm)
                           : groups == 1          ? (g.R + s.bm - 1) / s.bm
@@ -88,7 +102,7 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
             const double us = rounds * (std::ceil(stages / splits) * parts * s.stage * (0.75 + 0.25 * fill) + s.fixed) + join;
             if (us < least) {
                 least = us;
-                best.kind = whole ? s.kind : kAny;
+                best.kind = s.kind;
                 best.splits = splits;
                 best.kper = (int)((stages + splits - 1) / splits) * 64;
                 tiles(layout, g, s.bm, s.bn, &best);
@@ -98,19 +112,22 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
     }
     if (layout == kForward) {
         // Few rows: a workgroup reads nb rows of W at 24 bytes a ns and its rows
-        // of x, which are in L2, at 44.  The tiles' kernels cannot beat the
+        // of x, which are in L2, at 44; at 7.5 and 12 where rows are not on 16 bytes
+        // (16 rows of 2049 x 7167 in parts 1, 2, 4: 48, 70, 91 us; one of 513 x 7167
+        // 28, 17, 12).  The tiles' kernels cannot beat the
         // weights' bytes either.  Over parts 1, 2, 4: one row of 2048 x 7168 10.4,
         // 6.8, 6.8 us, 8 rows 12.6, 8.9, 12.4; one of 512 x 7168 10.2, 6.6, 4.7; one
         // of 16384 x 4096 22.8, 22.1, 23.2, 4 rows 24.2, 26.5, 33.4 (tiles 27.0), 16
         // rows 31.2, 45.8, 76.5 (tiles 27.5).  Groups of more than two rows, of
         // unknown evenness, are the tiles': 8 of 256 experts of 2048 x 2048, one row
         // each 17.4 (tiles 19.2), two 18.5 (19.1), four 28.1 (17.0).
+        const double w_rate = whole ? 24e3 : 7.5e3, x_rate = whole ? 44e3 : 12e3;
         least = std::max(least, 5 + (double)groups * g.N * g.K * 2 / 6e6 + (best.splits > 1 ? 7 : 0));
         for (int parts = 1; parts <= 4 && (g.E == 1 || rows <= 2); parts *= 2) {
             const int nb = 16 / parts, chunks = rows <= nb ? 1 : 4, per = nb * chunks;
             const double passes = std::ceil(rows / per), x = std::min(rows, (double)per);
             const double each = std::max(1.0, groups * std::ceil(g.N / (double)nb) * passes / cus);    // of a compute unit
-            const double us = 5 + each * g.K * 2 * (nb / 24e3 + x / 44e3);
+            const double us = 5 + each * g.K * 2 * (nb / w_rate + x / x_rate);
             GemmPlan few{};
             few.kind = kFew;
             few.splits = 1;

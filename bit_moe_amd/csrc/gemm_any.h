@@ -2,9 +2,10 @@
 // 128 x 128 tile (64 x 64 a wave); a stage of 64 of the contraction is loaded
 // into registers while the one before it is multiplied out of LDS.  Bound by
 // that way through the registers, 8 loads a thread and stage at addresses
-// tested one by one, and its LDS writes: 8192 x 2048 x 7168 in 358 us forward
-// (672 TFLOP/s), 380 as rows' gradient, 575 as weights' gradient, about twice
-// the time of rows on 16-byte addresses.
+// tested one by one, and its LDS writes: 8192 x 2048 x 7168 one element off
+// 16 bytes in 358 us forward (672 TFLOP/s), 380 as rows' gradient and 575 as
+// weights' gradient, 1.8, 1.75 and 2.9 times those of rows on 16-byte addresses;
+// where the widths are odd too (2049 x 7167) 453, 474 and 1314.
 #pragma once
 
 #include "gemm_util.h"
