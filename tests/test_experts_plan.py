@@ -1,10 +1,13 @@
 """The rule that chooses a product's kernel (experts_plan.cpp), on the CPU: what
-it takes against measured times."""
+it takes against measured times, and that the cases which are compared with
+float64 on the GPU reach every kernel."""
 import os
 import shutil
 import subprocess
 
 import pytest
+
+import _experts_cases as cases
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FORWARD, DX, DW = 0, 1, 2
@@ -66,3 +69,43 @@ def test_rows_of_any_alignment(plan, layout, R, N, K, parts, few):
     at = [1, 2, 4, 8, 16]
     took = few[at.index(p)] if kind == "few" else parts[at.index(splits)]
     assert took <= 1.4 * min(parts + few), (kind, splits, p, took)
+
+
+def whole(N, K, place, layout):
+    """Every row of the operands on 16 bytes (dense ones, from `place` on)."""
+    return place % 8 == 0 and K % 8 == 0 and (N % 8 == 0 or layout == FORWARD)
+
+
+def name(took):
+    kind, splits, parts, chunks = took
+    return f"{kind} {splits}" + (f" {parts} {chunks}" if kind == "few" else "")
+
+
+@pytest.mark.parametrize("layout,list_of", [(FORWARD, "FORWARD"), (DX, "DX"), (DW, "DW")])
+def test_cases_reach_every_kernel(plan, layout, list_of):
+    """The sizes that are compared with float64 take the kernels that they are
+    listed for, and no kernel that can be launched is missing."""
+    listed = getattr(cases, list_of)
+    for label, counts, N, K, place in listed:
+        took = plan(layout, len(counts), sum(counts), N, K, whole(N, K, place, layout))
+        assert name(took) == label, (counts, N, K, place, name(took))
+    kinds = {"256x256", "128x128", "any"} | ({"128x256", "64x128"} if layout != DW else set())
+    few = {f"few 1 {p} {c}" for p in (1, 2, 4) for c in (1, 4)} if layout == FORWARD else set()
+    labels = {c[0] for c in listed}
+    assert {c.split()[0] for c in labels} == kinds | ({"few"} if few else set())
+    assert few <= labels
+    assert {int(c.split()[1]) for c in labels} == {1, 2, 4, 8, 16}         # of each join, too
+    # groups of several experts, an empty one among them, in every kind
+    assert {c[0].split()[0] for c in listed if len(c[1]) > 1 and 0 in c[1]} >= kinds
+
+
+def test_backward_cases_reach_every_kernel(plan):
+    for dx, dw, T, N, K, pad, place in cases.BACKWARD:
+        on16 = lambda layout: whole(N, K, place, layout) and pad % 8 == 0  # noqa: E731
+        for layout, label in ((DX, dx), (DW, dw)):
+            took = plan(layout, 1, T, N, K, on16(layout), low=8)
+            assert name(took) == label, (layout, T, N, K, name(took))
+    assert {c[0].split()[0] for c in cases.BACKWARD} == {"256x256", "128x256", "128x128", "64x128", "any"}
+    assert {c[1].split()[0] for c in cases.BACKWARD} == {"256x256", "128x128", "any"}
+    for i in (0, 1):
+        assert {int(c[i].split()[1]) for c in cases.BACKWARD} == {1, 2, 4, 8, 16}

@@ -6,6 +6,7 @@ import math
 import pytest
 
 import _experts as ex
+import _experts_cases as cases
 from _gpu import require_gpu, say, torch
 
 pytestmark = pytest.mark.gpu
@@ -58,22 +59,15 @@ def dz_error(dz, dy, dtype):
     return ez + ex.half_ulp(dtype) ** 2 * (dz.abs() + ez) + 2.0 ** -35 * (dtype == HF)
 
 
-# T, N, K, padding between rows, place of the first element: few rows, odd sizes and addresses, parts of a tile's
-# stages, every tile size (test_experts_plan.py names them), contractions that are split
-BACKWARD = [(1, 64, 72, 0, 0), (3, 17, 33, 0, 0), (70, 200, 136, 8, 8), (130, 96, 100, 3, 1), (8192, 128, 64, 0, 0),
-            (1000, 1032, 264, 0, 0), (256, 8192, 136, 0, 0), (4096, 520, 7168, 0, 0), (2048, 2056, 2048, 0, 0),
-            (8200, 520, 1000, 0, 0), (513, 3000, 2500, 0, 0), (2050, 1003, 517, 0, 0)]
-
-
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("shape", BACKWARD, ids=str)
+@pytest.mark.parametrize("case", cases.BACKWARD, ids=str)
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
-def test_products_of_linear_backward_take_dz_whole(bm, act, shape, dtype):
-    T, N, K, pad, shift = shape
+def test_products_of_linear_backward_take_dz_whole(bm, act, case, dtype):
+    T, N, K, pad, shift = case[2:]
     g = torch.Generator().manual_seed(T + N + K)
     x, w = sparse(T, K, g, dtype), sparse(N, K, g, dtype)
     pre, dy = (torch.randn(T, N, generator=g) * 2).to(dtype), torch.randn(T, N, generator=g).to(dtype)
-    say(f"[experts] dz whole {act} {shape} {dtype}")
+    say(f"[experts] dz whole {act} {case} {dtype}")
     args = [padded(t, pad, shift) for t in (dy, x, w)]
     dx, dw, _ = bm.linear_backward(*args, act=act, pre=padded(pre, pad, 0), out_dtype=F32)
     dy, x, w = dy.cuda().double(), x.cuda().double(), w.cuda().double()         # (the oracle's products on the GPU)
