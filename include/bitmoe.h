@@ -490,7 +490,7 @@ typedef struct bitmoe_rows {
 
 typedef struct bitmoe_experts {
     void *data;            /* W_e[n][k] at element e * stride + n * ld + k */
-    int64_t ld, stride;    /* ld >= K; stride >= N * ld when E > 1 */
+    int64_t ld, stride;    /* ld >= K; stride >= (N - 1) * ld + K when E > 1 */
     int32_t E, N, K;
     int32_t dtype;
 } bitmoe_experts;

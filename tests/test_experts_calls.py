@@ -47,3 +47,14 @@ def test_backward_with_and_without_rounded_dz(act):
     assert back(act | 512) == EINVAL and back(5 | ex.ROUND_DZ) == EINVAL
     # the forward pass knows no such flag
     assert L.moe_linear(rows(n=0), experts(E=1), None, act | ex.ROUND_DZ, None, None, rows(n=0, cols=32), None, 0, None) == EINVAL
+
+
+def test_experts_apart_by_what_the_header_says():
+    """The least distance between experts that is accepted is the header's:
+    up to the last element, not to the end of a padded last row."""
+    assert re.search(r"ld >= K; stride >= \(N - 1\) \* ld \+ K when E > 1", open(HEADER).read())
+    L = bm.lib()
+    for n, k, ld in ((32, 16, 16), (32, 16, 24), (1, 16, 100)):
+        for less, rc in ((0, EWORKSPACE), (1, EINVAL)):
+            w = experts(N=n, K=k, ld=ld, stride=(n - 1) * ld + k - less)
+            assert L.moe_expert_matmul_dw(rows(cols=n), rows(cols=k), P, 8, w, 0, None, 0, None) == rc
