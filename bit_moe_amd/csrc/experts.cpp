@@ -25,7 +25,8 @@ int check_rows(const bitmoe_rows *m, int R, int cols, bool maps) {
     if (!m || m->rows < 0 || m->cols != cols || m->ld < m->cols) return BITMOE_EINVAL;
     if (!is16(m->dtype) && m->dtype != BITMOE_F32) return BITMOE_EINVAL;
     if (m->map ? (!maps || m->div < 1 || !aligned(m->map, 4)) : m->rows < R) return BITMOE_EINVAL;
-    if (R > 0 && (!m->data || !aligned(m->data, esize(m->dtype)))) return BITMOE_EINVAL;
+    // (a map may give rows of a matrix that has none: no address is needed)
+    if (R > 0 && (m->rows > 0 || !m->map) && (!m->data || !aligned(m->data, esize(m->dtype)))) return BITMOE_EINVAL;
     return BITMOE_OK;
 }
 

@@ -58,3 +58,14 @@ def test_experts_apart_by_what_the_header_says():
         for less, rc in ((0, EWORKSPACE), (1, EINVAL)):
             w = experts(N=n, K=k, ld=ld, stride=(n - 1) * ld + k - less)
             assert L.moe_expert_matmul_dw(rows(cols=n), rows(cols=k), P, 8, w, 0, None, 0, None) == rc
+
+
+def test_maps_over_a_matrix_without_rows():
+    """Every entry lies outside it: rows of zeros, nothing written.  No address
+    is asked for (torch gives none to a tensor without elements)."""
+    L = bm.lib()
+    none, w = dict(n=0, data=None, map=P), experts()
+    assert L.moe_expert_matmul_dw(rows(cols=32, **none), rows(), P, 8, w, 0, None, 0, None) == EWORKSPACE
+    assert L.moe_expert_matmul_dw(rows(cols=32), rows(**none), P, 8, w, 0, None, 0, None) == EWORKSPACE
+    for bad in (dict(n=0, data=None), dict(n=8, data=None, map=P), dict(n=8, data=P + 1, map=P)):
+        assert L.moe_expert_matmul_dw(rows(cols=32, **bad), rows(), P, 8, w, 0, None, 0, None) == EINVAL, bad

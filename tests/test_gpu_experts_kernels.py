@@ -126,3 +126,20 @@ def test_weights_gradient(bm, case, dtype, maps):
         within(acc[e], sums, b + 2.0 ** -23 * (sums.abs() + was[e].double().abs()), (ident(case), e, "accumulated"))
     for e in set(range(E)) - seen:
         assert (dw[e] == 0).all() and torch.equal(acc[e], was[e])
+
+
+@pytest.mark.parametrize("R,N,K", [(5, 64, 72), (300, 33, 17), (1, 2056, 264), (4000, 264, 512)])
+def test_maps_over_a_matrix_without_rows(bm, R, N, K):
+    E = 1 if R < 300 else 3
+    off = torch.tensor([0] + [R] * E, dtype=torch.int32).cuda()
+    w = torch.randn(E, N, K, device="cuda").to(BF)
+    rows = torch.arange(R, dtype=torch.int32, device="cuda")
+    none = lambda n: torch.empty(0, n, dtype=BF, device="cuda")  # noqa: E731
+    x, dy = torch.randn(R, K, device="cuda").to(BF), torch.randn(R, N, device="cuda").to(BF)
+    assert (bm.expert_matmul(none(K), w, off, x_rows=rows) == 0).all()
+    assert (bm.expert_matmul_dx(none(N), w, off, dy_rows=rows) == 0).all()
+    assert (bm.expert_matmul_dw(dy, none(K), off, x_rows=rows) == 0).all()
+    assert (bm.expert_matmul_dw(none(N), x, off, dy_rows=rows) == 0).all()
+    assert bm.expert_matmul(x, w, off, y_rows=rows, y=none(N)).shape == (0, N)
+    assert bm.expert_matmul_dx(dy, w, off, dx_rows=rows, dx=none(K)).shape == (0, K)
+    torch.cuda.synchronize()
