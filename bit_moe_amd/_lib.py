@@ -35,6 +35,7 @@ SYMBOLS = [
     "moe_cache_pool_bytes", "moe_cache_create", "moe_cache_layer", "moe_cache_map", "moe_cache_stats",
     "moe_cache_destroy",
     "moe_expert_matmul_workspace_bytes", "moe_expert_matmul", "moe_expert_matmul_dx", "moe_expert_matmul_dw",
+    "moe_expert_clear_ungrouped",
     "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward_workspace_bytes", "moe_linear_backward",
     "moe_swiglu", "moe_swiglu_backward", "moe_combine", "moe_combine_backward",
 ]
@@ -128,6 +129,7 @@ def _load(path: str) -> C.CDLL:
         "moe_expert_matmul": ([RP, EP, P, I, RP, P, SZ, P], I),
         "moe_expert_matmul_dx": ([RP, EP, P, I, RP, P, SZ, P], I),
         "moe_expert_matmul_dw": ([RP, RP, P, I, EP, I, P, SZ, P], I),
+        "moe_expert_clear_ungrouped": ([P, I, I, RP, P], I),
         "moe_linear_workspace_bytes": ([I, I, I], SZ),
         "moe_linear": ([RP, EP, P, I, RP, RP, RP, P, SZ, P], I),
         "moe_linear_backward_workspace_bytes": ([I, I, I], SZ),

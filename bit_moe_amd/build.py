@@ -17,7 +17,7 @@ LIB_CHECKED = os.path.join(HERE, "libbitmoe_checked.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.cpp", "plan.cpp", "cache.cpp", "dequant.hip", "route.hip", "bucket.hip", "decode.hip", "prefill.hip", "noalloc.hip", "quant.hip",
            "experts.cpp", "experts_plan.cpp", "experts_gemm.hip", "experts_fwd.hip", "experts_dx.hip", "experts_dw.hip",
-           "experts_rows.hip"]
+           "experts_rows.hip", "experts_share.cpp"]
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-Wno-unused-function", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 

@@ -91,6 +91,8 @@ struct ActBackward {
 int act_backward_slices(int T, int N);
 int launch_act_backward(const ActBackward &p, int dtype, hipStream_t s);
 
+// rows of c that the call's rows of no group go to: 0
+int launch_clear_ungrouped(const int32_t *offsets, int E, int R, const GemmRows &c, int cols, bool f32, hipStream_t s);
 int launch_swiglu(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows &h, int dtype, hipStream_t s);
 int launch_swiglu_backward(const bitmoe_rows &dh, const bitmoe_rows &gate, const bitmoe_rows &up,
                            const bitmoe_rows &dgate, const bitmoe_rows &dup, int dtype, hipStream_t s);

@@ -311,6 +311,21 @@ k_bias_grad(const float *partial, int slices, int N, void *db, int db_dtype) {
     }
 }
 
+// A row of c at a time for each of the call's rows outside the groups; where
+// there are none, a launch (3 us) and two loads a block.
+__global__ void __launch_bounds__(256)
+k_clear_ungrouped(const int32_t *offsets, int E, int R, GemmRows c, int cols, bool f32) {
+    const int first = min(max(offsets[0], 0), R), behind = max(min(max(offsets[E], 0), R), first);
+    for (int i = blockIdx.x; i < first + R - behind; i += gridDim.x) {
+        const int row = row_of(c, i < first ? i : behind + i - first);
+        if (row < 0) continue;
+        for (int n = threadIdx.x * 8; n < cols; n += 256 * 8) {
+            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            store8<BITMOE_BF16>(const_cast<void *>(c.p), (int64_t)row * c.ld + n, cols - n, f32, zero);
+        }
+    }
+}
+
 Mat mat(const bitmoe_rows *m) { return m ? Mat{m->data, m->ld} : Mat{nullptr, 0}; }
 
 // f(type, past) with both as constants
@@ -338,6 +353,12 @@ int with_k(int k, F f) {
 }  // namespace
 
 namespace bm_host {
+
+int launch_clear_ungrouped(const int32_t *offsets, int E, int R, const GemmRows &c, int cols, bool f32, hipStream_t s) {
+    k_clear_ungrouped<<<std::min(R, 2048), 256, 0, s>>>(offsets, E, R, c, cols, f32);
+    BM_LAUNCH_CHECK();
+    return BITMOE_OK;
+}
 
 int launch_swiglu(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows &h, int dtype, hipStream_t s) {
     const Grid2 g = pieces_grid(gate.rows, gate.cols);

@@ -174,11 +174,14 @@ def _expert_rows(op, a, w, offsets, a_rows, a_div, c_rows, c, out_dtype, ws, str
     ar = _rows(a, an, (None, n_in), a_rows, a_div)
     if a.dtype != w.dtype:
         raise ValueError(f"{an} must be of w's type")
+    ungrouped = c is None and c_rows is not None
     c = _output(c, (R, n_out), out_dtype or a.dtype, dev, cn, out_dtype)
     cr = _rows(c, cn, (None, n_out), c_rows, 1, f32=True)
     L = lib()
     hold, p, n = _scratch(ws, L.moe_expert_matmul_workspace_bytes(op, E, R, N, K), dev)
     s = _current_stream(dev)
+    if ungrouped:
+        _check(L.moe_expert_clear_ungrouped(offsets.data_ptr(), E, R, cr, s), "moe_expert_clear_ungrouped")
     if op == MATMUL:
         _check(L.moe_expert_matmul(ar, we, offsets.data_ptr(), R, cr, p, n, s), "moe_expert_matmul")
     else:
@@ -194,8 +197,10 @@ def expert_matmul(x, w, offsets, x_rows=None, x_div=1, y_rows=None, y=None, out_
     pair's token); y_rows int32 [R]: row r goes to y[y_rows[r]] (perm: pair
     order).  Without them row r is row r.  An entry outside the matrix reads as
     zeros, or is not written.  Returns y [R, N] in out_dtype (default x's;
-    float32 allowed); its rows that no group's row is written to are left as
-    they were, undefined where this call allocates y."""
+    float32 allowed).  Rows of y that no group's row is written to are left as
+    they were.  Where this call allocates y and y_rows is given, those that the
+    rows of no group go to are 0 (over a share of the experts, the other shares'
+    pairs: w[e0:e1], offsets[e0:e1 + 1]); without y_rows they are undefined."""
     return _expert_rows(MATMUL, x, w, offsets, x_rows, x_div, y_rows, y, out_dtype, ws, stream)
 
 

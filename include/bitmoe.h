@@ -522,6 +522,16 @@ int moe_expert_matmul_dw(const bitmoe_rows *dy, const bitmoe_rows *x, const int3
                          void *stream);
 
 /*
+ * A share of the experts (expert parallelism): moe_bucket's offsets from the
+ * share's first expert on, E + 1 of them, and its whole perm and R.  The rows
+ * before and behind the share's groups are other shares' pairs, whose rows of
+ * y (dx) the products leave as they were.  This sets those rows to 0, so that
+ * moe_combine adds nothing for them (0 times what an unwritten row holds may be
+ * NaN).  offsets, E, R and y (its map, or none) as for the product.
+ */
+int moe_expert_clear_ungrouped(const int32_t *offsets, int E, int R, const bitmoe_rows *y, void *stream);
+
+/*
  * Dense product with an epilogue (the shared expert's projections):
  *     z = x W^T + bias;  y = act(z) + residual
  * x [T][K], w with E = 1 [N][K], bias [N] of x's type or NULL, residual

@@ -9,7 +9,7 @@ import pytest
 
 import bit_moe_amd as bm
 from bit_moe_amd import experts as ex
-from bit_moe_amd._lib import BF16, EINVAL, EWORKSPACE, F16, F32, ExpertsStruct, RowsStruct
+from bit_moe_amd._lib import BF16, EINVAL, EUNSUPPORTED, EWORKSPACE, F16, F32, ExpertsStruct, RowsStruct
 
 P = 4096            # an aligned address that nothing dereferences
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "bitmoe.h")
@@ -69,3 +69,16 @@ def test_maps_over_a_matrix_without_rows():
     assert L.moe_expert_matmul_dw(rows(cols=32), rows(**none), P, 8, w, 0, None, 0, None) == EWORKSPACE
     for bad in (dict(n=0, data=None), dict(n=8, data=None, map=P), dict(n=8, data=P + 1, map=P)):
         assert L.moe_expert_matmul_dw(rows(cols=32, **bad), rows(), P, 8, w, 0, None, 0, None) == EINVAL, bad
+
+
+def test_clear_ungrouped_refusals():
+    L = bm.lib()
+
+    def call(off=P, E=4, R=8, **kw):
+        return L.moe_expert_clear_ungrouped(off, E, R, rows(**kw), None)
+    assert call(R=0, off=None, n=0, data=None) == 0
+    assert L.moe_expert_clear_ungrouped(P, 4, 8, None, None) == EINVAL
+    for bad in (dict(off=None), dict(off=P + 2), dict(E=0), dict(R=-1), dict(n=7), dict(ld=8), dict(dtype=7), dict(data=None),
+                dict(dtype=F32, data=P + 2), dict(map=P + 1), dict(map=P, div=0), dict(cols=0)):
+        assert call(**bad) == EINVAL, bad
+    assert call(E=1025) == EUNSUPPORTED and call(R=(1 << 24) + 1, n=1 << 25) == EUNSUPPORTED
