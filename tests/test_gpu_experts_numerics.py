@@ -175,3 +175,48 @@ def test_gelu_of_negative_values(bm, T, K):
         worst = over(db, want, 2.0 ** -14.8 * want.abs() + 2.0 ** -124)
         say(f"[experts] gelu's slope: largest error {worst:.2f} of its bound")
         assert worst <= 1
+
+
+@pytest.mark.parametrize("round_dz", [False, True])
+def test_linear_backward_captured_and_replayed(bm, round_dz):
+    """Two graphs of one call, with a workspace each from their own pools."""
+    T, N, K = 600, 264, 520
+    g = torch.Generator(device="cuda").manual_seed(3)
+    make = lambda *s: torch.empty(*s, dtype=BF, device="cuda").normal_(generator=g)  # noqa: E731
+    dy, x, w, pre = make(T, N), make(T, K), make(N, K), make(T, N)
+
+    def run():
+        return bm.linear_backward(dy, x, w, act="gelu", pre=pre, need_db=True, round_dz=round_dz)
+    run()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            graphs.append((graph, run()))
+    for _ in range(4):
+        for t in (dy, x, w, pre):
+            t.normal_(generator=g)
+        for graph, _ in graphs:
+            graph.replay()
+        want = run()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("R,N,K,pad", [(300, 72, 136, 0), (2048, 72, 72, 0), (300, 33, 17, 1), (3000, 264, 1032, 0)])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+def test_weights_gradient_added_to_16_bits(bm, R, N, K, pad, dtype):
+    """accumulate into the operands' type: the sum in float32, rounded once."""
+    g = torch.Generator().manual_seed(R + N)
+    dy, x = padded(torch.randn(R, N, generator=g).to(dtype), pad, 0), padded(torch.randn(R, K, generator=g).to(dtype), pad, 0)
+    was = (torch.randn(2, N, K, generator=g) * 30).to(dtype)
+    dw = was.cuda()
+    off = torch.tensor([0, R - 100, R], dtype=torch.int32).cuda()
+    assert bm.expert_matmul_dw(dy, x, off, dw=dw, accumulate=True) is dw
+    for e, s in ((0, slice(0, R - 100)), (1, slice(R - 100, R))):
+        d, v = dy[s].double(), x[s].double()
+        want, mag = was[e].cuda().double() + d.t() @ v, d.abs().t() @ v.abs()
+        assert over(dw[e], want, ex.half_ulp(dtype) * want.abs() + 1.01 * ex.sum_bound(R) * mag + 2.0 ** -22 *
+                    (want.abs() + was[e].cuda().double().abs()) + 2.0 ** -25 * (dtype == HF)) <= 1
