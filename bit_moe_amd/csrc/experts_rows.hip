@@ -4,7 +4,7 @@
 // of a row, reads every operand once and computes in fp32.  In bfloat16, cold:
 // SwiGLU's backward of 65536 x 2048 213 us (1.34 GB, 6.3 TB/s), combine of 8192 x 8
 // x 7168 onto a residual 195 (1.17 GB, 6.0), its backward 386 (2.0 GB, 5.2; half of
-// it writes), dz of 8192 x 2048 with db 27 + 6 us.  A plain copy runs at 5.0, so
+// it writes), dz of 8192 x 2048 in two parts with db 30 + 4 us.  A plain copy runs at 5.0, so
 // what is left is the launch and the last blocks' end.  8 rows of 2048 take 2.7
 // us, a launch.
 #include <algorithm>
@@ -312,7 +312,7 @@ k_bias_grad(const float *partial, int slices, int N, void *db, int db_dtype) {
 }
 
 // A row of c at a time for each of the call's rows outside the groups; where
-// there are none, a launch (3 us) and two loads a block.
+// there are none, a launch (3 to 6 us) and two loads a block.
 __global__ void __launch_bounds__(256)
 k_clear_ungrouped(const int32_t *offsets, int E, int R, GemmRows c, int cols, bool f32) {
     const int first = min(max(offsets[0], 0), R), behind = max(min(max(offsets[E], 0), R), first);
@@ -355,7 +355,7 @@ int with_k(int k, F f) {
 namespace bm_host {
 
 int launch_clear_ungrouped(const int32_t *offsets, int E, int R, const GemmRows &c, int cols, bool f32, hipStream_t s) {
-    k_clear_ungrouped<<<std::min(R, 2048), 256, 0, s>>>(offsets, E, R, c, cols, f32);
+    k_clear_ungrouped<<<std::min(R, 1024), 256, 0, s>>>(offsets, E, R, c, cols, f32);
     BM_LAUNCH_CHECK();
     return BITMOE_OK;
 }

@@ -19,9 +19,9 @@
 // with its loads left out).
 //
 // Bound by the matrix cores where K is long: 16384 x 4096 x 7168 in bfloat16
-// takes 672 us forward and as rows' gradient (1432 TFLOP/s), 694 as weights'
-// gradient; 8192^3 841, 768 and 788.  The matrix cores are busy 75% of the time
-// at about 1.65 GHz, the clock that their own power leaves.  Where K is short
+// takes 683 us forward, 685 as rows' gradient and 710 as weights' gradient (1409,
+// 1404, 1356 TFLOP/s); 8192^3 744, 753 and 775.  The matrix cores are busy 74% of
+// the time at about 1.6 GHz, the clock that their own power leaves.  Where K is short
 // the tile's ends show: a round of 256 x 256 tiles costs 9.5 us beside 1.35 us a
 // stage, most of it the epilogue's stores (an epilogue without LDS was no faster).  A workgroup stays
 // for several tiles and sends the next one's first stages off before the
@@ -127,7 +127,7 @@ BM_DEV s16x8 frag_at(uint32_t at, int i, int kk) {
 // MAPS (weights' gradient): the operands' rows are g.arows and g.brows (span32
 // is then of the whole operands).  PARTS (gradients): A is in two parts
 // (g.a_low); a tile takes all its stages over the low one, then, its sums scaled,
-// over the high one.
+// over the high one, in twice the time (8192 x 2048 x 7168 396 and 384 us).
 template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS, bool PARTS>
 __global__ void __launch_bounds__(64 * WM * WN)
 k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
