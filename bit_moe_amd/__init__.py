@@ -12,6 +12,9 @@ from ._lib import (BF16, BitMoEError, DECODE, ExpertCache, F32, FORMAT_2BIT, FOR
                    workspace_bytes)
 from .experts import (ACTS, MATMUL, MATMUL_DW, MATMUL_DX, combine, combine_backward, expert_matmul, expert_matmul_dw,
                       expert_matmul_dx, expert_matmul_workspace_bytes, linear, linear_backward, swiglu, swiglu_backward)
+from .rows8 import (BlockNormGrads, Rows8, block_norm, block_norm_backward, block_norm_backward_workspace_bytes,
+                    dequantize_rows, expert_matmul_i8, expert_matmul_i8_workspace_bytes, quantize_rows,
+                    swiglu_checkpoint, swiglu_checkpoint_backward, swiglu_rows8)
 
 
 def layer_from_canonical(H, I, E, k, router_bits, gate, up, down, grid, shared=None, device="cuda",
@@ -53,4 +56,7 @@ __all__ = ["ACTS", "BF16", "BitMoEError", "DECODE", "ExpertCache", "F32", "FORMA
            "quantize_mxfp4", "quantize_q2k", "lib", "pack_bf16", "pack_iq2x", "pack_mxfp4", "pack_q2k", "route", "route_workspace_bytes",
            "set_timing_events", "strerror", "topk", "version", "workspace_bytes",
            "MATMUL", "MATMUL_DW", "MATMUL_DX", "combine", "combine_backward", "expert_matmul", "expert_matmul_dw",
-           "expert_matmul_dx", "expert_matmul_workspace_bytes", "linear", "linear_backward", "swiglu", "swiglu_backward"]
+           "expert_matmul_dx", "expert_matmul_workspace_bytes", "linear", "linear_backward", "swiglu", "swiglu_backward",
+           "BlockNormGrads", "Rows8", "block_norm", "block_norm_backward", "block_norm_backward_workspace_bytes",
+           "dequantize_rows", "expert_matmul_i8", "expert_matmul_i8_workspace_bytes", "quantize_rows",
+           "swiglu_checkpoint", "swiglu_checkpoint_backward", "swiglu_rows8"]

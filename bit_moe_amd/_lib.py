@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbitmoe.so")
 LIB_CHECKED_PATH = os.path.join(HERE, "libbitmoe_checked.so")    # built with BITMOE_CHECK_IDS = 1
 
-F32, BF16, F16 = 0, 1, 2          # F16: the 16-bit expert layer (experts.py) only
+F32, BF16, F16, I8 = 0, 1, 2, 3   # F16: the 16-bit expert layer (experts.py) only; I8: codes (rows8.py)
 DECODE, PREFILL = 0, 1
 LAYOUT_CANONICAL, LAYOUT_TILED = 0, 1
 FORMAT_2BIT, FORMAT_MXFP4 = 0, 1
@@ -38,6 +38,9 @@ SYMBOLS = [
     "moe_expert_clear_ungrouped",
     "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward_workspace_bytes", "moe_linear_backward",
     "moe_swiglu", "moe_swiglu_backward", "moe_combine", "moe_combine_backward",
+    "moe_quantize_rows", "moe_dequantize_rows", "moe_expert_matmul_i8_workspace_bytes", "moe_expert_matmul_i8",
+    "moe_swiglu_rows8", "moe_swiglu_checkpoint", "moe_swiglu_checkpoint_backward",
+    "moe_block_norm", "moe_block_norm_backward_workspace_bytes", "moe_block_norm_backward",
 ]
 
 
@@ -57,6 +60,15 @@ class RowsStruct(C.Structure):
 class ExpertsStruct(C.Structure):
     _fields_ = [("data", C.c_void_p), ("ld", C.c_int64), ("stride", C.c_int64), ("E", C.c_int32),
                 ("N", C.c_int32), ("K", C.c_int32), ("dtype", C.c_int32)]
+
+
+class Rows8Struct(C.Structure):
+    _fields_ = [("q", RowsStruct), ("scale", C.c_void_p), ("ld_scale", C.c_int64), ("block", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class Experts8Struct(C.Structure):
+    _fields_ = [("q", ExpertsStruct), ("scale", C.c_void_p), ("scale_stride", C.c_int64)]
 
 
 _lib = None
@@ -92,9 +104,9 @@ def _load(path: str) -> C.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python -m bit_moe_amd.build`")
     L = C.CDLL(path)
-    P, I, I64, SZ = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
+    P, I, I64, SZ, F = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
     LP = C.POINTER(LayerStruct)
-    RP = EP = P            # bitmoe_rows and bitmoe_experts: a structure by reference, or its bytes
+    RP = EP = P            # bitmoe_rows, bitmoe_experts (and 8): a structure by reference, or its bytes
     sig = {
         "moe_route_workspace_bytes": ([LP, I, I], SZ),
         "moe_route": ([LP, P, I, I, P, P, P, P, SZ, P], I),
@@ -138,6 +150,16 @@ def _load(path: str) -> C.CDLL:
         "moe_swiglu_backward": ([RP, RP, RP, RP, RP, P], I),
         "moe_combine": ([RP, P, I, I, RP, RP, P], I),
         "moe_combine_backward": ([RP, RP, P, I, I, RP, P, P], I),
+        "moe_quantize_rows": ([RP, RP, P], I),
+        "moe_dequantize_rows": ([RP, RP, P], I),
+        "moe_expert_matmul_i8_workspace_bytes": ([I, I, I, I], SZ),
+        "moe_expert_matmul_i8": ([RP, EP, P, I, RP, P, SZ, P], I),
+        "moe_swiglu_rows8": ([RP, RP, RP, P], I),
+        "moe_swiglu_checkpoint": ([RP, RP, RP, RP, RP, P], I),
+        "moe_swiglu_checkpoint_backward": ([RP, RP, RP, RP, RP, RP, P], I),
+        "moe_block_norm": ([RP, P, RP, RP, F, RP, P, F, RP, P], I),
+        "moe_block_norm_backward_workspace_bytes": ([I, I], SZ),
+        "moe_block_norm_backward": ([RP, RP, RP, RP, P, RP, F, P, F, RP, RP, P, RP, P, I, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)

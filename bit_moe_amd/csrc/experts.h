@@ -53,6 +53,12 @@ struct GemmArgs {
     // A (not kForward, no map) as two 16-bit parts of a half of each value
     // (split16): the second's elements `a_low` further than the first's; 0: one
     int64_t a_low;
+    // products in 8 bits (launch_gemm_i8): a and b are codes; the sum is taken
+    // times a_scale[matrix row * a_ld_scale] and b_scale[e * b_scale_stride + n], or,
+    // with raw, left as the int32 it is (a part of a split contraction)
+    const float *a_scale, *b_scale;
+    int64_t a_ld_scale, b_scale_stride;
+    bool raw;
 };
 
 // How a product runs: which kernel, its tiles, into how many parts the

@@ -1,0 +1,157 @@
+// Products in 8 bits: their epilogue, and the kernel for codes of any alignment.
+#pragma once
+
+#include "gemm_util.h"
+
+namespace bm {
+
+// the scale of the call's row r (0 for one that the map does not give)
+BM_DEV float row_scale(const GemmArgs &g, int r) {
+    const int row = row_of(g.a, r);
+    return row >= 0 ? g.a_scale[row * g.a_ld_scale] : 0.f;
+}
+
+// The waves' int32 sums to memory, as tile_epilogue does it: a lane's 4 columns
+// of a row become 8 through LDS.  A value is (sum * row's scale) * column's
+// scale in fp32, rounded once to its type; the sum to fp32 is one rounding more
+// (from 2^24).  srow, sscale: output row (or -1) and scale of each of the tile's rows.
+template <int DT, int BM, int BN, int HALVES, int TM, int TN>
+BM_DEV void i8_epilogue(const GemmArgs &g, const f32x4 (&acc)[TM][TN], float *lds, const int *srow, const float *sscale,
+                        int e, int split, int n0, int m_at, int n_at, int wave, int lane) {
+    constexpr int MR = 16 * TM / HALVES, TH = TN / 2, CW = 16 * TH;      // columns at a time
+    constexpr int LDW = CW + 4, LPR = CW / 8, RPI = 64 / LPR, IT = 16 / RPI;
+    float *sw = lds + wave * epilogue_floats<TN>();
+    const int r0 = lane / LPR, c = (lane % LPR) * 8;
+    const int nn[2] = {n0 + n_at + c, n0 + n_at + c + (HALVES == 2 ? BN / 2 : CW)};
+    float cs[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            cs[h][j] = g.raw ? 1.f : g.b_scale[e * g.b_scale_stride + min(nn[h] + j, g.N - 1)];
+#pragma unroll
+    for (int q = 0; q < TM; q++) {
+        int rows[IT];
+        float rs[IT];
+#pragma unroll
+        for (int it = 0; it < IT; it++) {
+            const int m = 16 * q + it * RPI + r0, at = m / MR * (BM / 2) + m_at + m % MR;
+            rows[it] = srow[at];
+            rs[it] = sscale[at];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+#pragma unroll
+            for (int j = 0; j < TH; j++)
+                *reinterpret_cast<f32x4 *>(sw + (lane & 15) * LDW + 16 * j + 4 * (lane >> 4)) = acc[q][h * TH + j];
+            wave_together();
+#pragma unroll
+            for (int it = 0; it < IT; it++) {
+                const int r = it * RPI + r0;
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(sw + r * LDW + c + 4);
+                const int left = g.N - nn[h];
+                if (rows[it] < 0 || left <= 0) continue;
+                float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                const int64_t at = split * g.c_split + (int64_t)rows[it] * g.c.ld + nn[h];
+                if (!g.raw) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) v[j] = (float)__float_as_int(v[j]) * rs[it] * cs[h][j];
+                }
+                store8<DT - kI8>(const_cast<void *>(g.c.p), at, min(left, 8), g.c_f32, v);
+            }
+            wave_together();
+        }
+    }
+}
+
+struct __attribute__((packed, aligned(1))) C128 { uint32_t w[4]; };
+// 16 codes of a row (nullptr: zeros) from k, up to `end`
+BM_DEV uint4 load_codes(const uint8_t *row, int k, int end) {
+    if (!row || k >= end) return make_uint4(0, 0, 0, 0);
+    if (k + 16 <= end) {
+        const C128 u = *reinterpret_cast<const C128 *>(row + k);
+        return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; j++)
+        if (k + j < end) w[j >> 2] |= (uint32_t)row[k + j] << (8 * (j & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Codes of any alignment: a workgroup of 4 waves makes a 128 x 128 tile (64 x 64
+// a wave); a stage of 128 codes is loaded into registers while the one before it
+// is multiplied out of LDS (the layout is the 16-bit products': a code pair is an
+// element there).
+template <int DT>
+__global__ void __launch_bounds__(256)
+k_i8_any(GemmArgs g, int mtiles, int ntiles) {
+    constexpr int BM = 128, BN = 128, P = 4, TM = 4, TN = 4, STAGE = 2 * kBK;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[(BM + BN) * kBK];
+    static_assert(sizeof(lds) >= 4 * epilogue_floats<TN>() * 4, "");
+    __shared__ int srow[BM];
+    __shared__ float sscale[BM];
+    uint16_t *sa = lds, *sb = lds + BM * kBK;
+    Tile t;
+    Tiles<kForward, BM> list;
+    list.init(g, mtiles, ntiles * g.splits, blockIdx.x, gridDim.x);
+    if (!list.next(g, &t)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const Span k = span_of<kForward>(g, &t, ntiles);
+    const int m0 = t.m * BM, n0 = t.n * BN;
+    const uint8_t *A = static_cast<const uint8_t *>(g.a.p);
+    const uint8_t *B = static_cast<const uint8_t *>(g.b.p) + (int64_t)t.e * g.b_stride;
+    const uint8_t *arow[P], *brow[P];
+    int col[P];
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+        int r;
+        piece_at<true, BM>(tid + i * 256, &r, &col[i]);
+        const int row = t.r0 + m0 + r < t.r1 ? row_of(g.a, t.r0 + m0 + r) : -1;
+        arow[i] = row >= 0 ? A + (int64_t)row * g.a.ld : nullptr;
+        brow[i] = n0 + r < g.N ? B + (int64_t)(n0 + r) * g.b.ld : nullptr;
+    }
+    uint4 va[P], vb[P];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < P; i++) va[i] = load_codes(arow[i], k0 + 16 * col[i], k.end);
+#pragma unroll
+        for (int i = 0; i < P; i++) vb[i] = load_codes(brow[i], k0 + 16 * col[i], k.end);
+    };
+    set_rows<kForward, BM>(g, t, m0, tid, srow);
+    if (tid < BM) sscale[tid] = !g.raw && m0 + tid < t.r1 - t.r0 ? row_scale(g, t.r0 + m0 + tid) : 0.f;
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (k.beg < k.end) load(k.beg);
+    for (int k0 = k.beg; k0 < k.end; k0 += STAGE) {
+#pragma unroll
+        for (int i = 0; i < P; i++) *reinterpret_cast<uint4 *>(sa + (tid + i * 256) * 8) = va[i];
+#pragma unroll
+        for (int i = 0; i < P; i++) *reinterpret_cast<uint4 *>(sb + (tid + i * 256) * 8) = vb[i];
+        __syncthreads();
+        if (k0 + STAGE < k.end) load(k0 + STAGE);
+#pragma unroll
+        for (int kk = 0; kk < kBK; kk += 32) {
+            s16x8 fa[TM], fb[TN];
+#pragma unroll
+            for (int i = 0; i < TM; i++) fa[i] = frag<true, BM>(sa, wm * 64 + 16 * i, kk, lane);
+#pragma unroll
+            for (int j = 0; j < TN; j++) fb[j] = frag<true, BN>(sb, wn * 64 + 16 * j, kk, lane);
+#pragma unroll
+            for (int i = 0; i < TM; i++)
+#pragma unroll
+                for (int j = 0; j < TN; j++) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
+        }
+        __syncthreads();
+    }
+    __syncthreads();         // (srow, where the loop did not run)
+    i8_epilogue<DT, BM, BN, 1>(g, acc, reinterpret_cast<float *>(lds), srow, sscale, t.e, k.split, n0, wm * 64, wn * 64,
+                               wave, lane);
+}
+
+}  // namespace bm

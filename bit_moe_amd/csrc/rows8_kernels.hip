@@ -1,0 +1,411 @@
+// Rows in 8 bits: activations and weights into int8 codes with a scale for 32,
+// 64 or 128 columns or for the whole row, and back; the gated activation into
+// them, and with its inputs kept in them.
+//
+// A code is rint(127 x / m) for the block's largest magnitude m.  The quotient
+// has to be the correctly rounded one, because a tie (x = m / 2 gives 63.5) is
+// exact and common in 16 bits: an estimate t (1 / m), which may be an ulp off,
+// and one step on its exact remainder (an fma) give it for two more operations
+// than the estimate (q' = q + (t - q m) / m with 1 / m correctly rounded).  m and
+// x are first taken to m's own power of two, so nothing overflows on the way.
+// Every kernel is bound by memory.
+#include "rows8.h"
+#include "rows_util.h"
+
+namespace {
+
+using namespace bm;
+
+// ---- codes ----------------------------------------------------------------
+struct Coder {
+    float f, m, inv;        // x f = 127 x 2^-e, m 2^-e, its reciprocal
+    uint32_t keep;          // 0: the block's codes are 0
+};
+// of a block's largest magnitude (its bits, above infinity's for a NaN)
+BM_DEV Coder coder(uint32_t bits, float *scale) {
+    Coder k;
+    // 2^-e, at most 2^100 (what is smaller than 2^-100 need not reach 1)
+    const float to1 = __uint_as_float((uint32_t)min(max(254 - (int)(bits >> 23), 1), 227) << 23);
+    const float m = __uint_as_float(bits);
+    k.m = m * to1;
+    k.f = 127.f * to1;
+    k.inv = 1.f / k.m;
+    k.keep = bits != 0 && bits < 0x7F800000u ? 0xFFFFFFFFu : 0u;
+    // (at most what 127 times stays finite: fp32's largest value / 127, rounded down)
+    *scale = bits < 0x7F800000u ? fminf(m / 127.f, 0x1.0204060000000p+121f) : __uint_as_float(0x7FC00000u);
+    return k;
+}
+BM_DEV uint32_t max_bits(uint32_t m, float v) { return max(m, __float_as_uint(v) & 0x7FFFFFFFu); }
+BM_DEV uint32_t code_bits(const Coder &k, float x) {
+    const float t = x * k.f, q = t * k.inv;
+    // (the low byte of a value near 1.5 2^23 is that of the integer nearest to what was added)
+    return __float_as_uint(fmaf(fmaf(-q, k.m, t), k.inv, q) + 12582912.f);
+}
+BM_DEV uint32_t code4(const Coder &k, const float *x) {
+    const uint32_t lo = __builtin_amdgcn_perm(code_bits(k, x[1]), code_bits(k, x[0]), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code_bits(k, x[3]), code_bits(k, x[2]), 0x04000C0Cu);
+    return (lo | hi) & k.keep;
+}
+// the values of four codes
+BM_DEV void value4(uint32_t w, float scale, float *v) {
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = ((float)(w >> (8 * j) & 0xFFu) - 128.f) * scale;
+}
+
+struct __attribute__((packed, aligned(1))) B64 { uint32_t w[2]; };
+struct __attribute__((packed, aligned(1))) B128 { uint32_t w[4]; };
+// the first n (1 .. 4 W) codes of W words
+template <int W>
+BM_DEV void put_codes(int8_t *p, int n, const uint32_t (&w)[W]) {
+    if (n >= 4 * W) {
+        typename std::conditional<W == 4, B128, B64>::type u;
+#pragma unroll
+        for (int j = 0; j < W; j++) u.w[j] = w[j];
+        *reinterpret_cast<decltype(u) *>(p) = u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4 * W; j++)
+            if (j < n) p[j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
+    }
+}
+BM_DEV uint4 get_codes16(const int8_t *p, int n) {
+    if (n >= 16) {
+        const B128 u = *reinterpret_cast<const B128 *>(p);
+        return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; j++)
+        if (j < n) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+BM_DEV void values16(const uint4 &u, float scale, float (&v)[16]) {
+    value4(u.x, scale, v);
+    value4(u.y, scale, v + 4);
+    value4(u.z, scale, v + 8);
+    value4(u.w, scale, v + 12);
+}
+
+struct Rows8 {
+    int8_t *q;
+    float *scale;
+    int64_t ld, ld_scale;
+    int shift;              // log2 of the block, or 31: the row
+};
+
+// ---- blocks of columns ----------------------------------------------------
+// A thread takes 16 columns; the 2, 4 or 8 lanes of a block exchange their
+// largest magnitudes (all of them are there: a row's threads are a multiple of 8).
+template <int DT, bool F32>
+BM_DEV void load16v(const Mat &m, int64_t r, int c, int n, float (&v)[16]) {
+    load8<DT>(m.p, r * m.ld + c, n, F32, v);
+    load8<DT>(m.p, r * m.ld + c + 8, n - 8, F32, v + 8);
+}
+template <int DT>
+BM_DEV void store16v(const Mat &m, int64_t r, int c, int n, bool f32, const float (&v)[16]) {
+    store8<DT>(m.p, r * m.ld + c, n, f32, v);
+    if (n > 8) store8<DT>(m.p, r * m.ld + c + 8, n - 8, f32, v + 8);
+}
+template <int CTRL>
+BM_DEV uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
+}
+template <int SHIFT>
+BM_DEV uint32_t block_max(const float (&v)[16]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; j++) m = max_bits(m, v[j]);
+    m = dpp_max<0xB1>(m);                        // lane ^ 1
+    if (SHIFT >= 6) m = dpp_max<0x4E>(m);        // lane ^ 2
+    if (SHIFT >= 7) m = dpp_max<0x141>(m);       // the other four of eight
+    return m;
+}
+template <int SHIFT>
+BM_DEV void put_block(const Rows8 &q, int64_t r, int c, int n, const float (&v)[16]) {
+    float scale;
+    const Coder k = coder(block_max<SHIFT>(v), &scale);
+    const uint32_t w[4] = {code4(k, v), code4(k, v + 4), code4(k, v + 8), code4(k, v + 12)};
+    if (n > 0) put_codes(q.q + r * q.ld + c, n, w);
+    if ((c & ((1 << SHIFT) - 1)) == 0 && n > 0) q.scale[r * q.ld_scale + (c >> SHIFT)] = scale;
+}
+// body(row, column, how many of its 16 are there) for every thread of every
+// block of columns that has any
+template <int SHIFT, class F>
+BM_DEV void for_blocks(int rows, int cols, int cshift, F body) {
+    const int c = ((blockIdx.x << cshift) + (threadIdx.x & ((1 << cshift) - 1))) * 16;
+    const int step = gridDim.y * (256 >> cshift);
+    int r = blockIdx.y * (256 >> cshift) + (threadIdx.x >> cshift);
+    const int first = c & ~((1 << SHIFT) - 1);
+    if (first + (1 << SHIFT) <= cols) {
+        for (; r < rows; r += step) body(r, c, std::integral_constant<int, 16>{});
+    } else if (first < cols) {
+        for (; r < rows; r += step) body(r, c, min(max(cols - c, 0), 16));
+    }
+}
+
+template <int DT, bool F32, int SHIFT>
+__global__ void __launch_bounds__(256)
+k_quantize_blocks(Mat x, Rows8 q, int R, int C, int cshift) {
+    for_blocks<SHIFT>(R, C, cshift, [&](int r, int c, auto n) {
+        float v[16];
+        load16v<DT, F32>(x, r, c, n, v);
+        put_block<SHIFT>(q, r, c, n, v);
+    });
+}
+
+template <int DT, int SHIFT>
+__global__ void __launch_bounds__(256)
+k_swiglu_blocks(Mat gate, Mat up, Rows8 q, int R, int I, int cshift) {
+    for_blocks<SHIFT>(R, I, cshift, [&](int r, int c, auto n) {
+        float g[16], u[16];
+        load16v<DT, false>(gate, r, c, n, g);
+        load16v<DT, false>(up, r, c, n, u);
+#pragma unroll
+        for (int j = 0; j < 16; j++) g[j] = silu(g[j]) * u[j];
+        put_block<SHIFT>(q, r, c, n, g);
+    });
+}
+
+template <int DT, int SHIFT>
+__global__ void __launch_bounds__(256)
+k_swiglu_checkpoint(Mat gate, Mat up, Mat h, Rows8 gate8, Rows8 up8, int R, int I, int cshift) {
+    for_blocks<SHIFT>(R, I, cshift, [&](int r, int c, auto n) {
+        float g[16], u[16];
+        load16v<DT, false>(gate, r, c, n, g);
+        load16v<DT, false>(up, r, c, n, u);
+        put_block<SHIFT>(gate8, r, c, n, g);
+        put_block<SHIFT>(up8, r, c, n, u);
+#pragma unroll
+        for (int j = 0; j < 16; j++) g[j] = silu(g[j]) * u[j];
+        store16v<DT>(h, r, c, n, false, g);
+    });
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256)
+k_swiglu_checkpoint_backward(Mat dh, Rows8 gate8, Rows8 up8, Mat dgate, Mat dup, Mat h, int R, int I, int cshift) {
+    for_blocks<4>(R, I, cshift, [&](int r, int c, auto n) {
+        float d[16], g[16], u[16];
+        const uint4 cg = get_codes16(gate8.q + r * gate8.ld + c, n), cu = get_codes16(up8.q + r * up8.ld + c, n);
+        const float sg = gate8.scale[r * gate8.ld_scale + (c >> gate8.shift)];
+        const float su = up8.scale[r * up8.ld_scale + (c >> up8.shift)];
+        load16v<DT, false>(dh, r, c, n, d);
+        values16(cg, sg, g);
+        values16(cu, su, u);
+        // with p = 1 / (1 + e^-gate): dgate = dh up p (1 + gate (1 - p)), dup = dh gate p, h = gate p up
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const float p = 1.f / (1.f + __expf(-g[j])), v = g[j] * p;
+            g[j] = d[j] * u[j] * p * (1.f + g[j] * (1.f - p));
+            u[j] *= v;
+            d[j] *= v;
+        }
+        store16v<DT>(dgate, r, c, n, false, g);
+        store16v<DT>(dup, r, c, n, false, d);
+        if (h.p) store16v<DT>(h, r, c, n, false, u);
+    });
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256)
+k_dequantize(Rows8 q, Mat y, bool f32, int R, int C, int cshift) {
+    for_blocks<4>(R, C, cshift, [&](int r, int c, auto n) {
+        float v[16];
+        values16(get_codes16(q.q + r * q.ld + c, n), q.scale[r * q.ld_scale + (c >> q.shift)], v);
+        store16v<DT>(y, r, c, n, f32, v);
+    });
+}
+
+// ---- a scale for the row --------------------------------------------------
+// NT threads a row, 8 columns each and P times, kept in registers between the
+// maximum and the codes (P = 0: any number, made twice).
+template <int DT, bool F32>
+struct RowOf {
+    Mat x;
+    BM_DEV void get(int64_t r, int c, int n, float (&v)[8]) const { load8<DT>(x.p, r * x.ld + c, n, F32, v); }
+};
+template <int DT>
+struct SwigluOf {
+    Mat gate, up;
+    BM_DEV void get(int64_t r, int c, int n, float (&v)[8]) const {
+        float u[8];
+        load8<DT>(gate.p, r * gate.ld + c, n, false, v);
+        load8<DT>(up.p, r * up.ld + c, n, false, u);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = silu(v[j]) * u[j];
+    }
+};
+
+template <int NT, int P, class S>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT)
+k_rows8(S src, Rows8 q, int r0, int R, int C) {
+    constexpr int RPB = NT < 256 ? 256 / NT : 1, NW = NT / 64;
+    __shared__ uint32_t part[NW];
+    const int tid = threadIdx.x % NT;
+    const int64_t r = r0 + (int64_t)blockIdx.x * RPB + threadIdx.x / NT;
+    if (r >= R) return;                          // (whole waves; NT > 64: never)
+    constexpr int H = P ? P : 1;
+    float v[H][8];
+    uint32_t m = 0;
+    auto largest = [&](const float (&a)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) m = max_bits(m, a[j]);
+    };
+    if (P) {
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            const int c = (p * NT + tid) * 8;
+            if (c + 8 <= C) src.get(r, c, 8, v[p]);
+            else src.get(r, min(c, C - 1), max(C - c, 0), v[p]);
+        }
+#pragma unroll
+        for (int p = 0; p < P; p++) largest(v[p]);
+    } else {
+        for (int c = tid * 8; c < C; c += NT * 8) {
+            src.get(r, c, C - c, v[0]);
+            largest(v[0]);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
+    if (NW > 1) {
+        if ((tid & 63) == 0) part[tid >> 6] = m;
+        __syncthreads();
+        m = part[0];
+#pragma unroll
+        for (int w = 1; w < NW; w++) m = max(m, part[w]);
+    }
+    float scale;
+    const Coder k = coder(m, &scale);
+    auto codes = [&](int c, const float (&a)[8]) {
+        const uint32_t w[2] = {code4(k, a), code4(k, a + 4)};
+        put_codes(q.q + r * q.ld + c, C - c, w);
+    };
+    if (P) {
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            const int c = (p * NT + tid) * 8;
+            if (c < C) codes(c, v[p]);
+        }
+    } else {
+        for (int c = tid * 8; c < C; c += NT * 8) {
+            src.get(r, c, C - c, v[0]);
+            codes(c, v[0]);
+        }
+    }
+    if (tid == 0) q.scale[r * q.ld_scale] = scale;
+}
+
+// ---- launches -------------------------------------------------------------
+Mat mat(const bitmoe_rows *m) { return m ? Mat{m->data, m->ld} : Mat{nullptr, 0}; }
+Rows8 rows8(const bitmoe_rows8 &m) {
+    const int shift = m.block == 32 ? 5 : m.block == 64 ? 6 : m.block == 128 ? 7 : 31;
+    return Rows8{static_cast<int8_t *>(m.q.data), m.scale, m.q.ld, m.ld_scale, shift};
+}
+
+template <int NT, int P, class S>
+int rows8_by(const S &src, const Rows8 &q, int R, int C, hipStream_t s) {
+    constexpr int RPB = NT < 256 ? 256 / NT : 1;
+    constexpr int most = 1 << 21;               // (a launch holds less than 2^32 threads)
+    for (int r0 = 0; r0 < R; r0 += most) {
+        k_rows8<NT, P, S><<<(std::min(R - r0, most) + RPB - 1) / RPB, NT < 256 ? 256 : NT, 0, s>>>(src, q, r0, std::min(R, r0 + most), C);
+        BM_LAUNCH_CHECK();
+    }
+    return BITMOE_OK;
+}
+// A wave a row where there are rows enough and its registers hold one.
+template <class S>
+int rows8_of(const S &src, const Rows8 &q, int R, int C, hipStream_t s) {
+    if (C > 32768) return rows8_by<1024, 0>(src, q, R, C, s);
+    if (C > 8192) return rows8_by<1024, 4>(src, q, R, C, s);
+    if (R < 1024 && C > 2048) return rows8_by<1024, 1>(src, q, R, C, s);
+    if (R < 1024 && C > 512) return rows8_by<256, 1>(src, q, R, C, s);
+    if (C > 4096) return rows8_by<256, 4>(src, q, R, C, s);
+    if (C > 2048) return rows8_by<64, 8>(src, q, R, C, s);
+    if (C > 1024) return rows8_by<64, 4>(src, q, R, C, s);
+    return rows8_by<64, 2>(src, q, R, C, s);
+}
+
+// f(SHIFT) of the block
+template <class F>
+int with_shift(int block, F f) {
+    if (block == 32) return f(std::integral_constant<int, 5>{});
+    if (block == 64) return f(std::integral_constant<int, 6>{});
+    return f(std::integral_constant<int, 7>{});
+}
+template <class F>
+int with_type(int dtype, F f) {
+    return dtype == BITMOE_BF16 ? f(std::integral_constant<int, BITMOE_BF16>{}) : f(std::integral_constant<int, BITMOE_F16>{});
+}
+
+}  // namespace
+
+namespace bm_host {
+
+int launch_quantize_rows(const bitmoe_rows &x, const bitmoe_rows8 &q, hipStream_t s) {
+    const Rows8 out = rows8(q);
+    return with_type(x.dtype, [&](auto dt) {
+        constexpr int DT = dt.value;
+        auto go = [&](auto f32) {
+            constexpr bool F = decltype(f32)::value;
+            if (q.block == 0) return rows8_of(RowOf<DT, F>{mat(&x)}, out, x.rows, x.cols, s);
+            return with_shift(q.block, [&](auto sh) {
+                const Grid2 g = pieces_grid(x.rows, x.cols, 16, 3);
+                k_quantize_blocks<DT, F, sh.value><<<g.grid, 256, 0, s>>>(mat(&x), out, x.rows, x.cols, g.cshift);
+                BM_LAUNCH_CHECK();
+                return BITMOE_OK;
+            });
+        };
+        if (DT == BITMOE_F16 && x.dtype == BITMOE_F32) return go(std::true_type{});
+        return go(std::false_type{});
+    });
+}
+
+int launch_dequantize_rows(const bitmoe_rows8 &q, const bitmoe_rows &y, hipStream_t s) {
+    return with_type(y.dtype, [&](auto dt) {
+        const Grid2 g = pieces_grid(q.q.rows, q.q.cols, 16, 3);
+        k_dequantize<dt.value><<<g.grid, 256, 0, s>>>(rows8(q), mat(&y), y.dtype == BITMOE_F32, q.q.rows, q.q.cols, g.cshift);
+        BM_LAUNCH_CHECK();
+        return BITMOE_OK;
+    });
+}
+
+int launch_swiglu_rows8(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows8 &q, hipStream_t s) {
+    return with_type(gate.dtype, [&](auto dt) {
+        if (q.block == 0) return rows8_of(SwigluOf<dt.value>{mat(&gate), mat(&up)}, rows8(q), gate.rows, gate.cols, s);
+        const Grid2 g = pieces_grid(gate.rows, gate.cols, 16, 3);
+        return with_shift(q.block, [&](auto sh) {
+            k_swiglu_blocks<dt.value, sh.value><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), rows8(q), gate.rows, gate.cols, g.cshift);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        });
+    });
+}
+
+int launch_swiglu_checkpoint(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows &h,
+                             const bitmoe_rows8 &gate8, const bitmoe_rows8 &up8, hipStream_t s) {
+    const Grid2 g = pieces_grid(gate.rows, gate.cols, 16, 3);
+    return with_type(gate.dtype, [&](auto dt) {
+        return with_shift(gate8.block, [&](auto sh) {
+            k_swiglu_checkpoint<dt.value, sh.value><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), mat(&h), rows8(gate8),
+                                                                         rows8(up8), gate.rows, gate.cols, g.cshift);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        });
+    });
+}
+
+int launch_swiglu_checkpoint_backward(const bitmoe_rows &dh, const bitmoe_rows8 &gate8, const bitmoe_rows8 &up8,
+                                      const bitmoe_rows &dgate, const bitmoe_rows &dup, const bitmoe_rows *h,
+                                      hipStream_t s) {
+    const Grid2 g = pieces_grid(dh.rows, dh.cols, 16, 3);
+    return with_type(dh.dtype, [&](auto dt) {
+        k_swiglu_checkpoint_backward<dt.value><<<g.grid, 256, 0, s>>>(mat(&dh), rows8(gate8), rows8(up8), mat(&dgate),
+                                                                     mat(&dup), mat(h), dh.rows, dh.cols, g.cshift);
+        BM_LAUNCH_CHECK();
+        return BITMOE_OK;
+    });
+}
+
+}  // namespace bm_host

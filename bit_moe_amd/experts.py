@@ -27,10 +27,14 @@ _DTYPES = {}
 
 
 def _dtype(t, what, f32=False):
+    return _dtype_code(t.dtype, what, f32)
+
+
+def _dtype_code(dtype, what, f32=False):
     if not _DTYPES:
         torch = _torch()
         _DTYPES.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
-    code = _DTYPES.get(t.dtype)
+    code = _DTYPES.get(dtype)
     if code is None or (code == F32 and not f32):
         raise TypeError(f"{what} must be bfloat16 or float16" + (" or float32" if f32 else ""))
     return code

@@ -586,6 +586,131 @@ int moe_combine_backward(const bitmoe_rows *dy, const bitmoe_rows *o, const floa
                          const bitmoe_rows *d_o, float *dw, void *stream);
 
 /*
+ * The 16-bit expert layer's rows in 8 bits: what serves it with half the
+ * weights' bytes and twice the matrix cores' rate, and keeps a training step's
+ * activations in half their bytes.
+ *
+ * A row is int8 codes and float32 scales, one for `block` columns (the last
+ * block of a row may be shorter) or, with block 0, one for the whole row.  For
+ * the values x of a block and m their largest magnitude
+ *     scale = m / 127,  code = rint(127 x / m)   (ties to even),
+ * so a code stands for code * scale, within scale / 2 of x (m >= 2^-110,
+ * below which the scale's own rounding shows), and is -127 .. 127.
+ * A block of zeros has scale 0; scale is rounded down where code * scale would be
+ * infinite (m the largest float32); one that holds an infinity or NaN has scale NaN
+ * and codes 0 (it stands for NaN throughout).  127 x / m is rounded to float32
+ * once before rint, which for 16-bit x never changes a code.
+ *
+ * Conventions are those of the 16-bit expert layer above (sizes, maps, streams,
+ * workspaces, errors), and:
+ *  - Codes have any address and any ld >= cols (in bytes); rows on 16-byte
+ *    addresses with whole 16-byte pieces run fastest.  Scales are aligned to 4.
+ *  - block is 0, 32, 64 or 128.  Block b of row i has its scale at scale[i *
+ *    ld_scale + b]; ld_scale >= the blocks of a row.
+ *  - Outputs must not overlap inputs.  Columns between cols and ld are not written.
+ */
+#define BITMOE_I8 3 /* dtype of q */
+
+typedef struct bitmoe_rows8 {
+    bitmoe_rows q;         /* the codes; map and div as there, for the scales too */
+    float *scale;
+    int64_t ld_scale;
+    int32_t block;
+    int32_t reserved;      /* 0 */
+} bitmoe_rows8;
+
+typedef struct bitmoe_experts8 {
+    bitmoe_experts q;      /* the codes of W_e[n][k] */
+    const float *scale;    /* of row n of W_e at element e * scale_stride + n */
+    int64_t scale_stride;  /* >= N when E > 1 */
+} bitmoe_experts8;
+
+/*
+ * Rows of x (BITMOE_BF16, BITMOE_F16 or BITMOE_F32, no map) into 8 bits, and
+ * back into rows y of any of these types: y = code * scale in float32, then y's type.  The
+ * rows are x's (q's); q (y) has at least as many.  No rows: nothing is done.
+ */
+int moe_quantize_rows(const bitmoe_rows *x, const bitmoe_rows8 *q, void *stream);
+int moe_dequantize_rows(const bitmoe_rows8 *q, const bitmoe_rows *y, void *stream);
+
+/*
+ * moe_expert_matmul in 8 bits: for the rows r of expert e's group
+ *     y[r][n] = (sum_k x[r][k] W_e[n][k]) * scale of x[r] * scale of W_e[n]
+ * with both operands' codes, the sum in int32 (exact) and the two products in
+ * float32, in this order.  x: block 0, K columns, a map or none; y: N columns of
+ * BITMOE_BF16, BITMOE_F16 or BITMOE_F32.  K < 2^17 (EUNSUPPORTED), where no sum
+ * leaves int32.  offsets NULL (E = 1): one group of all R rows.  Codes of -128
+ * are taken as such.  A row that x's map does not give reads as codes of 0
+ * and a scale of 0.  Else as moe_expert_matmul, moe_expert_clear_ungrouped too.
+ * ws: moe_expert_matmul_i8_workspace_bytes(E, R, N, K).
+ */
+size_t moe_expert_matmul_i8_workspace_bytes(int E, int R, int N, int K);
+int moe_expert_matmul_i8(const bitmoe_rows8 *x, const bitmoe_experts8 *w, const int32_t *offsets, int R,
+                         const bitmoe_rows *y, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The gated activation into 8 bits, for a down projection in 8 bits: the rows
+ * of h = silu(gate) up in float32, never rounded to 16 bits.  gate, up [R][I] of
+ * one 16-bit type, q [R][I].  No maps.
+ */
+int moe_swiglu_rows8(const bitmoe_rows *gate, const bitmoe_rows *up, const bitmoe_rows8 *q, void *stream);
+
+/*
+ * The gated activation whose inputs a training step keeps in 8 bits.  The
+ * forward call is moe_swiglu and, of what it read, gate and up into 8 bits (not
+ * block 0); the backward call is moe_swiglu_backward with gate and up as the
+ * codes stand for them, and, for the down projection's weights' gradient, their
+ * h again if its pointer is not NULL.  All [R][I]; gate8 and up8 may be the
+ * halves of one [R][2I] matrix; dgate, dup and h of dh's type; dgate, dup or h
+ * may be dh itself (same address and ld).  No maps.
+ */
+int moe_swiglu_checkpoint(const bitmoe_rows *gate, const bitmoe_rows *up, const bitmoe_rows *h,
+                          const bitmoe_rows8 *gate8, const bitmoe_rows8 *up8, void *stream);
+int moe_swiglu_checkpoint_backward(const bitmoe_rows *dh, const bitmoe_rows8 *gate8, const bitmoe_rows8 *up8,
+                                   const bitmoe_rows *dgate, const bitmoe_rows *dup, const bitmoe_rows *h,
+                                   void *stream);
+
+/*
+ * The norms around a block (the layer, or another): the norm of the block's
+ * output o, its gate, the residual stream with its scale, and the norm before the
+ * next block, in one pass.  With rms(v) = sqrt(mean of v^2 over the row + eps)
+ *     s = scale residual + gate * (o / rms(o) * w_after)
+ *     n = s / rms(s) * w_before
+ * o, gate, n [T][H] and w_after, w_before [H] of one 16-bit type; residual, s
+ * [T][H] of that type or BITMOE_F32.  gate has T rows, or one for all tokens.
+ * Left out by NULL: o (with it gate and w_after: s = scale residual, the norm
+ * before the first block), residual (0), a weight (1), gate (1), n (the norm
+ * after the last block) and s; of o and n one is there, of o and residual one, of
+ * s and n one.  n is the norm of s in float32, before s is rounded to its type.
+ * eps >= 1e-30; H <= 16384 (EUNSUPPORTED); no maps.  s may be the residual
+ * itself and n may be o itself (same address and ld, type).
+ *
+ * Backward, given ds (the gradient of s from the stream's later uses, or NULL)
+ * and dn (or NULL), s where dn is given and o where the forward call had it:
+ *     t = ds + (the gradient of s through the norm before)
+ *     dresidual = scale t;  d_o;  dgate;  dw_after, dw_before (sums over tokens)
+ * each written if its pointer is not NULL.  dn, d_o of the 16-bit type, ds and
+ * dresidual of that type or BITMOE_F32, dw_after and dw_before [H] of dw_dtype
+ * (that type or BITMOE_F32); dgate [T][H] of the 16-bit type for a gate of T
+ * rows, [1][H] of that type or BITMOE_F32 for a gate of one row (summed over
+ * tokens).  Where the
+ * forward call had no w_after (w_before) its sum is the gradient at ones.
+ * dresidual may be ds itself, d_o may be o or dn itself, and dgate [T][H] may be
+ * the gate itself (same address and ld, type).  T = 0: the sums are 0.
+ * ws: moe_block_norm_backward_workspace_bytes(T, H), 256-byte aligned (for any of
+ * the outputs).
+ */
+int moe_block_norm(const bitmoe_rows *o, const void *w_after, const bitmoe_rows *gate, const bitmoe_rows *residual,
+                   float scale, const bitmoe_rows *s, const void *w_before, float eps, const bitmoe_rows *n,
+                   void *stream);
+size_t moe_block_norm_backward_workspace_bytes(int T, int H);
+int moe_block_norm_backward(const bitmoe_rows *dn, const bitmoe_rows *ds, const bitmoe_rows *s, const bitmoe_rows *o,
+                            const void *w_after, const bitmoe_rows *gate, float scale, const void *w_before,
+                            float eps, const bitmoe_rows *d_o, const bitmoe_rows *dresidual, void *dw_after,
+                            const bitmoe_rows *dgate, void *dw_before, int dw_dtype, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/*
  * Measurement hook.  When start and stop are both hipEvent_t handles (passed
  * as void*), every later decode or prefill FFN call made from the calling
  * thread launches one kernel with hipExtLaunchKernel and these events, which
