@@ -12,7 +12,7 @@ namespace bm {
 
 template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS = false, bool PARTS = false>
 int launch_tile(const GemmArgs &g, const bm_host::GemmPlan &p, hipStream_t s) {
-    constexpr int lds = TileLds<LAY, BM, BN, WM, WN, MAPS>::bytes;
+    constexpr int lds = TileLds<LAY, DT, BM, BN, WM, WN, MAPS>::bytes;
     // LDS above 64 KiB must be opted into per kernel and device
     static std::atomic<uint64_t> opted{0};
     int dev = 0;

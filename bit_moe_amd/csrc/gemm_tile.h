@@ -35,6 +35,7 @@
 
 #include <type_traits>
 
+#include "gemm_i8.h"
 #include "gemm_util.h"
 
 namespace bm {
@@ -82,13 +83,14 @@ BM_DEV void phase_barrier() {
 
 // Dynamic LDS of a workgroup: two stages; the output rows of this tile and the
 // next; A's rows; for the weights' gradient a ring of row maps (64 of A's, 64 of
-// B's, four stages); the epilogue's part, which is its own, so that the next
+// B's, four stages); in 8 bits the rows' scales; the epilogue's part, which is its own, so that the next
 // tile's first stages can be on their way during it.
-template <int LAY, int BM, int BN, int WM, int WN, bool MAPS>
+template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS>
 struct TileLds {
     static constexpr int rows = 2 * (BM + BN) * kBK * 2;
     static constexpr int maps = rows + 3 * BM * 4;
-    static constexpr int out = maps + (MAPS ? 4 * 128 * 4 : 0);
+    static constexpr int scales = maps + (MAPS ? 4 * 128 * 4 : 0);
+    static constexpr int out = scales + (DT >= kI8 ? 2 * BM * 4 : 0);
     static constexpr int bytes = out + WM * WN * epilogue_floats<BN / WN / 16>() * 4;
     static_assert(bytes <= 160 * 1024, "");
 };
@@ -135,6 +137,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     constexpr int PA = UM * kBK / 8 / (64 * NW), PB = UN * kBK / 8 / (64 * NW);   // a unit's loads per wave
     constexpr int TI = UM / WM / 16, TJ = UN / WN / 16;                    // 16 x 16 products of a wave in a quadrant
     constexpr bool AKC = LAY != kGradWeights, BKC = LAY == kForward;
+    static_assert(LAY == kForward || DT < kI8, "");
     static_assert((LAY == kGradWeights || !MAPS) && (LAY == kForward || MAPS ? !PARTS : true), "");
     constexpr int kUA = UM * kBK, kUB = UN * kBK, kStage = 2 * (kUA + kUB);       // elements
     static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW, "");
@@ -160,8 +163,9 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     // stage, by addresses made one by one, with the zero piece for what is not
     // there.  Rows past the group, and columns past the matrix, read its last
     // row (first columns): their results are not stored.
-    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::rows);
+    int *srow = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, DT, BM, BN, WM, WN, MAPS>::rows);
     int *xrow = srow + 2 * BM;
+    float *sscale = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, DT, BM, BN, WM, WN, MAPS>::scales);
     int m0, n0, kbeg, kend, split, stages, whole;  // whole: whole stages
     const uint16_t *A, *B, *abase, *bbase;         // the matrices; what stage 0 goes by
     uint32_t aoff[AKC ? 2 * PA : PA + 2], boff[BKC ? 2 * PB : PB + 2];   // bytes: KC by half and piece;
@@ -225,13 +229,15 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         abase = wave_ptr(abase);
         bbase = wave_ptr(bbase);
         set_rows<LAY, BM>(g, t, m0, tid, srow + par * BM);
+        if (DT >= kI8 && tid < BM)
+            sscale[par * BM + tid] = !g.raw && m0 + tid < t.r1 - t.r0 ? row_scale(g, t.r0 + m0 + tid) : 0.f;
     };
     // MAPS: the rows that the maps give (g.arows, g.brows), fetched two stages
     // before the loads that go by them; a stage's offsets are made at the
     // operand's first unit and kept for its second.  Every wave fetches them
     // all, to the same place (the same values), and so waits only for its own
     // loads.
-    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::maps);
+    int *maps = reinterpret_cast<int *>(reinterpret_cast<char *>(lds) + TileLds<LAY, DT, BM, BN, WM, WN, MAPS>::maps);
     const uint32_t maps_at = lds_addr(maps);
     auto fetch_map = [&](const int32_t *rows, int s, int b) {
         dma4(rows + t.r0 + min(s * kBK + lane, kend - 1), maps_at + ((s & 3) * 128 + b * 64) * 4);
@@ -295,7 +301,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     };
     constexpr int kLoads = PA > PB ? PA : PB;
 
-    f32x4 acc[2 * TI][2 * TJ];
+    Acc<DT> acc[2 * TI][2 * TJ];
     s16x8 ra0[2][TI], ra1[2][TI], rb0[2][TJ], rb1[2][TJ];       // [half of the stage's contraction]
     static_assert((TI & (TI - 1)) == 0 && (TJ & (TJ - 1)) == 0 && kUA % 512 == 0 && kUB % 512 == 0, "frag_at");
     uint32_t a_at = frag_place<AKC, UM>(lds_addr(lds), wm * (UM / WM), lane);
@@ -385,7 +391,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
 #pragma unroll
             for (int i = 0; i < 2 * TI; i++)
 #pragma unroll
-                for (int j = 0; j < 2 * TJ; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < 2 * TJ; j++) acc[i][j] = Acc<DT>{0, 0, 0, 0};
         }
         if (stages > 0) {
             phase_barrier<3 * PA + 3 * PB + 2 * MAPS>();
@@ -421,7 +427,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
             __syncthreads();       // xrow; srow, where no stage was
         }
         if (more) begin();
-        if (PARTS) {
+        if constexpr (PARTS) {
             const float scale = again ? 1.f / low_scale<DT>() : 2.f;
 #pragma unroll
             for (int i = 0; i < 2 * TI; i++)
@@ -430,9 +436,13 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         }
         low = PARTS && !again;
         if (again) continue;
-        tile_epilogue<LAY, DT, BM, BN, 2>(
-            g, acc, reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, BM, BN, WM, WN, MAPS>::out),
-            srow + par * BM, e, part, n, wm * (UM / WM), wn * (UN / WN), wave, lane);
+        float *through = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, DT, BM, BN, WM, WN, MAPS>::out);
+        if constexpr (DT >= kI8)
+            i8_epilogue<DT, BM, BN, 2>(g, acc, through, srow + par * BM, sscale + par * BM, e, part, n, wm * (UM / WM),
+                                       wn * (UN / WN), wave, lane);
+        else
+            tile_epilogue<LAY, DT, BM, BN, 2>(g, acc, through, srow + par * BM, e, part, n, wm * (UM / WM),
+                                              wn * (UN / WN), wave, lane);
         if (!more) return;
         par ^= 1;
     }

@@ -2,6 +2,8 @@
 // matrix-core operands, the search for a workgroup's tile, the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "experts.h"
 
@@ -23,15 +25,15 @@ constexpr int kBK = 64;             // contraction per stage
 
 // ---- elements -------------------------------------------------------------
 // DT: BITMOE_BF16 or BITMOE_F16; for products in 8 bits kI8 + the output's type:
-// 16 codes in the place of 8 elements, the sums' int32 in that of their float32
+// 16 codes in the place of 8 elements, sums in int32
 constexpr int kI8 = 16;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 template <int DT>
-BM_DEV f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
+using Acc = typename std::conditional<(DT >= kI8), i32x4, f32x4>::type;
+template <int DT>
+BM_DEV Acc<DT> mfma16(s16x8 a, s16x8 b, Acc<DT> c) {
     if constexpr (DT >= kI8)
-        return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                                             __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
-                                             __builtin_bit_cast(i32x4, c), 0, 0, 0));
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
     else if constexpr (DT == BITMOE_BF16)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b),
                                                        c, 0, 0, 0);

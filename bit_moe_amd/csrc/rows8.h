@@ -33,6 +33,9 @@ int launch_swiglu_checkpoint_backward(const bitmoe_rows &dh, const bitmoe_rows8 
 
 // y = W x in 8 bits: kForward with a and b codes, in elements (bytes) of which
 // the strides and K are counted too, and their scales.  out: the outputs' type.
+// The kernels are the 16-bit products': two codes lie where an element lies there.
+GemmPlan i8_plan(const GemmArgs &g, bool whole);
+bool i8_whole(const GemmArgs &g);            // every row begins on 16 bytes and has whole 16-byte pieces
 size_t i8_ws_bytes(int E, int R, int N, int K);
 int launch_gemm_i8(int out, const GemmArgs &g, void *ws, hipStream_t s);
 
