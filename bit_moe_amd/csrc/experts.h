@@ -71,10 +71,13 @@ struct GemmPlan {
     int64_t grid;       // workgroups that would take one tile each
     int parts, chunks;  // kFew: its P and NC
     size_t ws;          // bytes: the parts' float32, then (kGradWeights) the rows of both maps
+    bool pack;          // 8 bits: the operands' rows are laid on 16 bytes first (behind the parts in ws)
 };
 // every row begins on a 16-byte address and has whole 8-element pieces
 bool gemm_whole(int layout, const GemmArgs &g);
 GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole);
+// the row and column tiles and the grid of tiles of bm x bn (p->splits parts)
+void plan_tiles(int layout, const GemmArgs &g, int bm, int bn, GemmPlan *p);
 // workspace of a product of these sizes, whatever its addresses
 size_t gemm_ws_bytes(int layout, const GemmArgs &g);
 int launch_gemm(int layout, int dtype, const GemmArgs &g, void *ws, hipStream_t s);

@@ -9,6 +9,33 @@ namespace {
 using namespace bm;
 using bm_host::GemmPlan;
 
+// Rows of K codes at any address to rows of ld, whole 16-byte pieces with zeros
+// behind K, at `to`: the call's rows of x (with their scales) that lie in a group,
+// and the rows of W of the experts that have some.  A wave a row.
+__global__ void __launch_bounds__(256)
+k_i8_pack(GemmArgs g, uint8_t *x, float *scale, uint8_t *w, int ld) {
+    const int lane = threadIdx.x & 63, r0 = group_start(g, 0), r1 = group_start(g, g.E);
+    const int64_t last = g.R + (int64_t)g.E * g.N, step = (int64_t)gridDim.x * 4;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < last; i += step) {
+        const uint8_t *from;
+        uint8_t *to;
+        if (i < g.R) {
+            const int r = (int)i;
+            if (r < r0 || r >= r1) continue;
+            const int row = row_of(g.a, r);
+            from = row >= 0 ? static_cast<const uint8_t *>(g.a.p) + (int64_t)row * g.a.ld : nullptr;
+            to = x + (int64_t)r * ld;
+            if (lane == 0) scale[r] = row >= 0 ? g.a_scale[row * g.a_ld_scale] : 0.f;
+        } else {
+            const int e = (int)((i - g.R) / g.N), n = (int)(i - g.R - (int64_t)e * g.N);
+            if (group_start(g, e + 1) <= group_start(g, e)) continue;
+            from = static_cast<const uint8_t *>(g.b.p) + (int64_t)e * g.b_stride + (int64_t)n * g.b.ld;
+            to = w + (i - g.R) * ld;
+        }
+        for (int k = lane * 16; k < ld; k += 64 * 16) *reinterpret_cast<uint4 *>(to + k) = load_codes(from, k, g.K);
+    }
+}
+
 template <int DT, int P>
 void few(const GemmArgs &g, const GemmPlan &p, hipStream_t s) {
     if (p.chunks == 1) k_i8_few<DT, P, 1><<<(int)p.grid, 256, 0, s>>>(g, p.mt, p.nt);
@@ -47,6 +74,21 @@ template <int DT>
 int launch_of(const GemmArgs &args, void *ws, hipStream_t s) {
     const GemmPlan p = bm_host::i8_plan(args, bm_host::i8_whole(args));
     GemmArgs g = args;
+    if (p.pack) {
+        const bm_host::I8Pack k = bm_host::i8_pack(g.E, g.R, g.N, g.K);
+        char *at = static_cast<char *>(ws) + p.ws - k.bytes;
+        uint8_t *x = reinterpret_cast<uint8_t *>(at + k.x), *w = reinterpret_cast<uint8_t *>(at + k.w);
+        float *scale = reinterpret_cast<float *>(at + k.scale);
+        const int64_t rows = g.R + (int64_t)g.E * g.N;
+        k_i8_pack<<<(int)std::min<int64_t>((rows + 3) / 4, 1 << 16), 256, 0, s>>>(g, x, scale, w, (int)k.ld);
+        BM_LAUNCH_CHECK();
+        g.a = GemmRows{x, nullptr, k.ld, g.R, 0, 0, false};
+        g.b = GemmRows{w, nullptr, k.ld, g.N, 0, 0, false};
+        g.b_stride = (int64_t)g.N * k.ld;
+        g.a_scale = scale;
+        g.a_ld_scale = 1;
+        g.K = (int)k.ld;
+    }
     g.splits = p.splits;
     g.kper = p.kper;
     if (p.splits == 1) return product<DT>(g, p, s);

@@ -54,7 +54,9 @@ const Shape kAnyShapes[] = {
     {kAny, 128, 128, 2, 4.50, 4.0},
 };
 
-void tiles(int layout, const GemmArgs &g, int bm, int bn, GemmPlan *p) {
+}  // namespace
+
+void plan_tiles(int layout, const GemmArgs &g, int bm, int bn, GemmPlan *p) {
     p->nt = (g.N + bn - 1) / bn;
     if (layout == kGradWeights) {
         p->mt = (g.M + bm - 1) / bm;
@@ -64,8 +66,6 @@ void tiles(int layout, const GemmArgs &g, int bm, int bn, GemmPlan *p) {
         p->grid = ((int64_t)p->mt * p->nt * p->splits + 7) / 8 * 8;
     }
 }
-
-}  // namespace
 
 bool gemm_whole(int layout, const GemmArgs &g) {
     if (layout == kGradWeights) return on16(g.a.p, g.a.ld, g.M) && on16(g.b.p, g.b.ld, g.N);
@@ -105,7 +105,7 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
                 best.kind = s.kind;
                 best.splits = splits;
                 best.kper = (int)((stages + splits - 1) / splits) * 64;
-                tiles(layout, g, s.bm, s.bn, &best);
+                plan_tiles(layout, g, s.bm, s.bn, &best);
                 best.ws = splits == 1 ? 0 : ((size_t)out * 4 * splits + 255) / 256 * 256;
             }
         }
@@ -133,7 +133,7 @@ GemmPlan gemm_plan(int layout, const GemmArgs &g, bool whole) {
             few.splits = 1;
             few.parts = parts;
             few.chunks = chunks;
-            tiles(layout, g, per, nb, &few);
+            plan_tiles(layout, g, per, nb, &few);
             if (us < least && few.grid < 1 << 24) {                // (a launch holds less than 2^32 threads)
                 least = us;
                 best = few;

@@ -65,13 +65,14 @@ BM_DEV void i8_epilogue(const GemmArgs &g, const i32x4 (&acc)[TM][TN], float *ld
 }
 
 struct __attribute__((packed, aligned(1))) C128 { uint32_t w[4]; };
+BM_DEV uint4 code_piece(const uint8_t *p) {
+    const C128 u = *reinterpret_cast<const C128 *>(p);
+    return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+}
 // 16 codes of a row (nullptr: zeros) from k, up to `end`
 BM_DEV uint4 load_codes(const uint8_t *row, int k, int end) {
     if (!row || k >= end) return make_uint4(0, 0, 0, 0);
-    if (k + 16 <= end) {
-        const C128 u = *reinterpret_cast<const C128 *>(row + k);
-        return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
-    }
+    if (k + 16 <= end) return code_piece(row + k);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 16; j++)
@@ -186,20 +187,16 @@ k_i8_few(GemmArgs g, int mtiles, int ntiles) {
     };
     // U steps of 128: where every lane's codes are there, its loads are issued
     // together
-    auto whole = [](const uint8_t *p) __attribute__((always_inline)) {
-        const C128 u = *reinterpret_cast<const C128 *>(p);
-        return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
-    };
     auto load = [&](int b, Batch &o) __attribute__((always_inline)) {
         const int k = kb + b * (128 * U);
         if (__all(k + 128 * (U - 1) + 32 <= kend)) {
 #pragma unroll
-            for (int u = 0; u < 2 * U; u++) o.w[u] = whole(w + k + (u >> 1) * 128 + (u & 1) * 16);
+            for (int u = 0; u < 2 * U; u++) o.w[u] = code_piece(w + k + (u >> 1) * 128 + (u & 1) * 16);
 #pragma unroll
             for (int c = 0; c < NC; c++) {
                 if (x[c]) {
 #pragma unroll
-                    for (int u = 0; u < 2 * U; u++) o.x[c][u] = whole(x[c] + k + (u >> 1) * 128 + (u & 1) * 16);
+                    for (int u = 0; u < 2 * U; u++) o.x[c][u] = code_piece(x[c] + k + (u >> 1) * 128 + (u & 1) * 16);
                 } else {
 #pragma unroll
                     for (int u = 0; u < 2 * U; u++) o.x[c][u] = make_uint4(0, 0, 0, 0);
@@ -256,6 +253,27 @@ k_i8_few(GemmArgs g, int mtiles, int ntiles) {
     }
 }
 
+// The expert of the call's row r, the last whose rows do not begin behind it: one
+// after another, or, where r is the wave's and all its lanes are there, by all of
+// them at once (a search's loads wait for each other).
+BM_DEV int expert_of(const GemmArgs &g, int r) {
+    int e = 0;
+    for (int hi = g.E; hi - e > 1;) {
+        const int mid = (e + hi) / 2;
+        if (group_start(g, mid) <= r) e = mid;
+        else hi = mid;
+    }
+    return e;
+}
+BM_DEV int wave_expert(const GemmArgs &g, int r) {
+    int n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+        const int e = e0 + lane_id();
+        n += __popcll(__ballot(e < g.E && group_start(g, e) <= r));
+    }
+    return n - 1;
+}
+
 // The parts' int32 sums (exact), scaled as in i8_epilogue.  NS parts' loads are
 // issued together.
 template <int DT, int NS>
@@ -263,19 +281,13 @@ __global__ void __launch_bounds__(256)
 k_i8_join(GemmArgs g, const float *part, int cshift) {
     const int per = 256 >> cshift, n = ((blockIdx.x << cshift) + (threadIdx.x & ((1 << cshift) - 1))) * 8;
     const int left = min(g.N - n, 8);
-    if (left <= 0) return;
     const int begin = group_start(g, 0), end = group_start(g, g.E);
     const int64_t step = (int64_t)g.R * g.N;
     for (int r = begin + blockIdx.y * per + (threadIdx.x >> cshift); r < end; r += gridDim.y * per) {
+        // (before a lane leaves: all of the wave's count)
+        const int e = g.E == 1 ? 0 : cshift >= 6 ? wave_expert(g, r) : expert_of(g, r);
         const int row = row_of(g.c, r);
-        if (row < 0) continue;
-        // the row's expert: the last whose rows do not begin behind it
-        int e = 0;
-        for (int hi = g.E; hi - e > 1;) {
-            const int mid = (e + hi) / 2;
-            if (group_start(g, mid) <= r) e = mid;
-            else hi = mid;
-        }
+        if (row < 0 || left <= 0) continue;
         int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int s0 = 0; s0 < g.splits; s0 += NS) {              // (splits is a multiple of NS)
             float o[NS][8];

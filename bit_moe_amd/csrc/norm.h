@@ -32,7 +32,7 @@ struct NormBackArgs {
     int32_t T, H;
     void *dwa, *dwb, *dg;                   // sums over tokens [H], of dw_dtype; dg: for a gate of one row, of dg_dtype
     int32_t dw_dtype, dg_dtype;
-    float *partial;                         // [slices][3][H]
+    float *partial;                         // [slices][2][H]
 };
 int norm_slices(int T, int H);
 int launch_block_norm_backward(const NormBackArgs &a, int dtype, hipStream_t st);

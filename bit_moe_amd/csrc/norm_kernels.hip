@@ -3,10 +3,10 @@
 // and their gradients.  With p = w_b dn, t = ds + b (p - s b^2 <p, s> / H) and
 // v = g t w_a:  dr = scale t,  do = a (v - o a^2 <v, o> / H),
 //   dw_a = sum t g o a,  dg = t o a w_a,  dw_b = sum dn s b.
-// One workgroup takes a row, each thread 8 of its columns (P times), which stay
-// in registers from the sums to the outputs.  The backward pass needs all its sums
-// in one step: <v, o> is taken apart into <g w_a o, ds>, <g w_a o, p> and
-// <g w_a o, s>, which do not need t.  Bound by memory.
+// A row is taken by as many threads as it has 8 columns (16 where it is wider
+// than 8192), and stays in their registers from the sums to the outputs.  The
+// backward pass needs all its sums in one step: <v, o> is taken apart into
+// <g w_a o, ds>, <g w_a o, p> and <g w_a o, s>, which do not need t.
 #include "norm.h"
 #include "rows_util.h"
 
@@ -19,24 +19,35 @@ using bm_host::NormMat;
 
 constexpr int kMost = 16;           // waves of a workgroup
 
-// Sums of N values over a workgroup's row, the lanes by a tree, the waves in
-// order; every thread has them.  part: LDS that no other reduction uses between
-// the same two barriers.
+// A wave's sum by lane moves alone (shuffles go through LDS), in every lane: rows
+// of 16 lanes, then 15 and 47 onto the next row, 31 onto the upper half.
+template <int CTRL, int ROWS>
+BM_DEV float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, ROWS == 0xF));
+}
+BM_DEV float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
+BM_DEV float wave_total(float v) {
+    v = dpp_add<0x142, 0xA>(row16_sum(v));
+    return lane_of(dpp_add<0x143, 0xC>(v), 63);
+}
+// Sums of N values over the `nw` waves of a row, the waves' by a tree too; every
+// thread has them.  put before a barrier, get behind it.
 template <int N>
-BM_DEV void row_sums(float (&v)[N], float (*part)[N]) {
-    const int nw = blockDim.x >> 6;
+BM_DEV void put_sums(float (&v)[N], float (*part)[8], int wave) {
 #pragma unroll
-    for (int i = 0; i < N; i++) v[i] = wave_sum(v[i]);
-    if (nw == 1) return;
-    if ((threadIdx.x & 63) == 0)
+    for (int i = 0; i < N; i++) v[i] = wave_total(v[i]);
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-        for (int i = 0; i < N; i++) part[threadIdx.x >> 6][i] = v[i];
-    __syncthreads();
+        for (int i = 0; i < N; i++) part[wave][i] = v[i];
+    }
+}
+template <int N>
+BM_DEV void get_sums(float (&v)[N], const float (*part)[8], int nw) {
+    const int w = threadIdx.x & 15;
 #pragma unroll
-    for (int i = 0; i < N; i++) v[i] = part[0][i];
-    for (int w = 1; w < nw; w++)
+    for (int i = 0; i < N; i++) v[i] = w < nw ? part[w][i] : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; i++) v[i] += part[w][i];
+    for (int i = 0; i < N; i++) v[i] = lane_of(row16_sum(v[i]), 15);
 }
 
 // 1 / rms of a row whose values are taken times f
@@ -61,7 +72,7 @@ BM_DEV void load_m(const NormMat &m, int64_t r, int c, int n, float missing, flo
 template <int DT, int P>
 __global__ void __launch_bounds__(1024)
 k_block_norm(NormArgs a) {
-    __shared__ float part[4][kMost][1];
+    __shared__ float part[4][kMost][8];
     const int64_t r = blockIdx.x;
     const int step = blockDim.x * 8;
     float v[P][8], o[P][8];
@@ -79,7 +90,9 @@ k_block_norm(NormArgs a) {
         for (int p = 0; p < P; p++)
 #pragma unroll
             for (int j = 0; j < 8; j++) s[0] = fmaf(x[p][j] * f, x[p][j] * f, s[0]);
-        row_sums<1>(s, part[k]);
+        put_sums<1>(s, part[k], threadIdx.x >> 6);
+        if (blockDim.x > 64) __syncthreads();
+        get_sums<1>(s, part[k], blockDim.x >> 6);
         return s[0];
     };
 #pragma unroll
@@ -118,120 +131,260 @@ k_block_norm(NormArgs a) {
     }
 }
 
-// A workgroup's rows one after another; the sums over tokens stay in its
-// registers and end as one slice of the partial sums.
-template <int DT, int P>
+// ---- backward -------------------------------------------------------------
+// eight values of a row as they are in memory; WIDE: the row may be float32
+template <bool WIDE>
+struct Piece {
+    uint4 lo, hi;
+};
+template <int DT, bool WIDE>
+BM_DEV void fetch(const NormMat &m, int64_t r, int c, int n, Piece<WIDE> &q) {
+    q.lo = make_uint4(0, 0, 0, 0);
+    if (WIDE) q.hi = make_uint4(0, 0, 0, 0);
+    if (!m.p || n <= 0) return;
+    if (WIDE && m.f32) {
+        float v[8];
+        load8<DT>(m.p, r * m.ld + c, n, true, v);
+        q.lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        q.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(m.p) + r * m.ld + c;
+        q.lo = n >= 8 ? load16(p) : load16_part(p, n);
+    }
+}
+template <int DT, bool WIDE>
+BM_DEV void unpack(const Piece<WIDE> &q, bool f32, float (&v)[8]) {
+    if (WIDE && f32) {
+        const uint32_t w[8] = {q.lo.x, q.lo.y, q.lo.z, q.lo.w, q.hi.x, q.hi.y, q.hi.z, q.hi.w};
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
+    } else {
+        values<DT>(q.lo, v);
+    }
+}
+
+// a value that the compiler takes for a new one
+BM_DEV void hold(uint4 &q) { asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w)); }
+
+// A workgroup is `groups` rows of `nt` threads each, and takes its rows one after
+// another, the next ones' values on their way meanwhile.  What is summed over
+// tokens stays in registers (a gate of one row and w_a leave one sum, of t o a: dw_a
+// is it times g, dg it times w_a) and ends as one slice of the partial sums.  One
+// barrier a row: what it separates alternates between two places (three for
+// `far`, which also has to be cleared).
+template <int DT, int P, bool WIDE, bool TOKEN>
 __global__ void __launch_bounds__(1024)
-k_block_norm_backward(NormBackArgs a) {
-    __shared__ float part[2][kMost][6];
-    const int step = blockDim.x * 8;
-    auto col = [&](int p) { return (int)threadIdx.x * 8 + p * step; };
-    auto left = [&](int p) { return min(max(a.H - col(p), 0), 8); };
-    auto at = [&](int p) { return min(col(p), a.H - 1); };
-    float wa[P][8], wb[P][8], da[P][8], dg[P][8], db[P][8];
+k_block_norm_backward(NormBackArgs a, int nt, int groups) {
+    __shared__ float part[3][kMost][8];
+    __shared__ int far[3];
+    extern __shared__ float joined[];
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / nt), tid = threadIdx.x - group * nt;   // (nt: whole waves)
+    const int nw = nt >> 6, wave = threadIdx.x >> 6, first = group * nw;
+    auto col = [&](int p) { return (tid + p * nt) * 8; };
+    auto left = [&](int p) { return min(a.H - col(p), 8); };
+    // g w_a (w_a alone for a gate by token); w_b stays as it is in memory
+    float wa[P][8], sa[P][8], sb[P][8];
+    uint4 wb[P];
 #pragma unroll
-    for (int p = 0; p < P; p++)
+    for (int p = 0; p < P; p++) {
+        const int c = min(col(p), a.H - 1), n = max(left(p), 0);
+        float g[8];
+        load_w<DT>(a.wa, c, n, wa[p]);
+        load_w<DT>(TOKEN ? nullptr : a.gate.p, c, n, g);
+        const uint32_t one = elem_pair<DT>(1.f, 1.f);
+        wb[p] = make_uint4(one, one, one, one);
+        if (a.wb) {
+            const uint16_t *w = static_cast<const uint16_t *>(a.wb) + c;
+            wb[p] = n >= 8 ? load16(w) : load16_part(w, n);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; j++) da[p][j] = dg[p][j] = db[p][j] = 0.f;
-    for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x) {
-        float dn[P][8], ds[P][8], s[P][8], o[P][8], g[P][8];
+        for (int j = 0; j < 8; j++) {
+            wa[p][j] *= g[j];
+            sa[p][j] = sb[p][j] = 0.f;
+        }
+    }
+    if (threadIdx.x < 3) far[threadIdx.x] = 0;
+    __syncthreads();
+    struct Row {
+        Piece<false> dn, o, g;
+        Piece<WIDE> ds, s;
+    };
+    Row ahead[P];
+    const int64_t step = (int64_t)gridDim.x * groups;
+    auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
         for (int p = 0; p < P; p++) {
-            load_m<DT>(a.dn, r, at(p), left(p), 0.f, dn[p]);
-            load_m<DT>(a.ds, r, at(p), left(p), 0.f, ds[p]);
-            load_m<DT>(a.s, r, at(p), left(p), 0.f, s[p]);
-            load_m<DT>(a.o, r, at(p), left(p), 0.f, o[p]);
-            load_m<DT>(a.gate, r, at(p), left(p), 1.f, g[p]);
-            load_w<DT>(a.wa, at(p), left(p), wa[p]);
-            load_w<DT>(a.wb, at(p), left(p), wb[p]);
+            const int n = r < a.T ? left(p) : 0;
+            fetch<DT>(a.dn, r, col(p), n, ahead[p].dn);
+            fetch<DT>(a.o, r, col(p), n, ahead[p].o);
+            fetch<DT>(a.s, r, col(p), n, ahead[p].s);
+            fetch<DT>(a.ds, r, col(p), n, ahead[p].ds);
+            if (TOKEN) fetch<DT>(a.gate, r, col(p), n, ahead[p].g);
         }
-        // s and o times fs and fo
+    };
+    load((int64_t)blockIdx.x * groups + group);
+    int turn = 0, three = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.T; r0 += step) {
+        const int64_t r = r0 + group;
+        Row row[P];
+#pragma unroll
+        for (int p = 0; p < P; p++) row[p] = ahead[p];
+        load(r + step);
+        // (the row's values stay as they are in memory: half the registers, unpacked twice)
         float q[6], fs = 1.f, fo = 1.f;
-        auto sums = [&](int k) {
+        auto sums = [&]() __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < 6; i++) q[i] = 0.f;
 #pragma unroll
-            for (int p = 0; p < P; p++)
+            for (int p = 0; p < P; p++) {
+                float dn[8], ds[8], s[8], o[8], g[8], w[8];
+                unpack<DT>(row[p].dn, false, dn);
+                unpack<DT>(row[p].o, false, o);
+                unpack<DT>(row[p].s, a.s.f32, s);
+                unpack<DT>(row[p].ds, a.ds.f32, ds);
+                if (TOKEN) unpack<DT>(row[p].g, false, g);
+                values<DT>(wb[p], w);
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    const float x = s[p][j], y = o[p][j], d = wb[p][j] * dn[p][j], u = g[p][j] * wa[p][j] * y;
+                    const float x = s[j] * fs, y = o[j] * fo, d = w[j] * dn[j];
+                    const float u = (TOKEN ? g[j] * wa[p][j] : wa[p][j]) * y;
                     q[0] = fmaf(x, x, q[0]);
                     q[1] = fmaf(d, x, q[1]);
                     q[2] = fmaf(y, y, q[2]);
-                    q[3] = fmaf(u, ds[p][j], q[3]);
+                    q[3] = fmaf(u, ds[j], q[3]);
                     q[4] = fmaf(u, d, q[4]);
                     q[5] = fmaf(u, x, q[5]);
                 }
-            row_sums<6>(q, part[k]);
+            }
         };
-        sums(0);
-        if (!(q[0] < INFINITY && q[2] < INFINITY)) {
-            fs = q[0] < INFINITY ? 1.f : kDown;
-            fo = q[2] < INFINITY ? 1.f : kDown;
-#pragma unroll
-            for (int p = 0; p < P; p++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    s[p][j] *= fs;
-                    o[p][j] *= fo;
-                }
-            sums(1);
+        sums();
+        put_sums<6>(q, part[turn], wave);
+        // squares' sums that may leave fp32 (16 waves' stay below 2^120)
+        if (!(q[0] < 0x1p116f && q[2] < 0x1p116f)) far[three] = 1;
+        const int next = three == 2 ? 0 : three + 1;
+        if (threadIdx.x == 0) far[next] = 0;
+        __syncthreads();
+        get_sums<6>(q, part[turn] + first, nw);
+        if (far[three]) {
+            fs = q[0] < 0x1p120f ? 1.f : kDown;
+            fo = q[2] < 0x1p120f ? 1.f : kDown;
+            sums();
+            put_sums<6>(q, part[2], wave);
+            __syncthreads();
+            get_sums<6>(q, part[2] + first, nw);
+            __syncthreads();
         }
+        turn ^= 1;
+        three = next;
         // (with the factors: s and o by their own, b and a are fs b', fo a')
         const float b1 = inv_rms(q[0], a.H, a.eps, fs), a1 = inv_rms(q[2], a.H, a.eps, fo);
         const float b = a.dn.p ? fs * b1 : 0.f, mean = b1 * q[1] / (float)a.H;             // of p and s b
         const float vo = q[3] + b * (q[4] - b1 * mean * q[5]), ra = fo * a1, mo = a1 * vo / (float)a.H;
+        if (r >= a.T) continue;
+        // (unpacked anew, which the compiler would not do by itself)
 #pragma unroll
         for (int p = 0; p < P; p++) {
-            float t[8], d_o[8], u[8];
+            hold(row[p].dn.lo);
+            hold(row[p].o.lo);
+            hold(row[p].s.lo);
+            hold(row[p].ds.lo);
+            if (TOKEN) hold(row[p].g.lo);
+            hold(wb[p]);
+        }
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            float dn[8], ds[8], s[8], o[8], g[8], w[8];
+            unpack<DT>(row[p].dn, false, dn);
+            unpack<DT>(row[p].o, false, o);
+            unpack<DT>(row[p].s, a.s.f32, s);
+            unpack<DT>(row[p].ds, a.ds.f32, ds);
+            if (TOKEN) unpack<DT>(row[p].g, false, g);
+            values<DT>(wb[p], w);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const float sn = s[p][j] * b1, on = o[p][j] * a1;
-                t[j] = a.dn.p ? fmaf(b, wb[p][j] * dn[p][j] - sn * mean, ds[p][j]) : ds[p][j];
-                const float gt = g[p][j] * t[j];
-                d_o[j] = ra * (gt * wa[p][j] - on * mo);
-                u[j] = t[j] * on * wa[p][j];
-                if (a.dn.p) db[p][j] = fmaf(dn[p][j], sn, db[p][j]);
-                da[p][j] = fmaf(gt, on, da[p][j]);
-                dg[p][j] += u[j];
-                t[j] *= a.scale;
+                const float sn = s[j] * fs * b1, on = o[j] * fo * a1;
+                // (where there is no dn, s, sn and dn are 0, and b)
+                const float t = fmaf(b, w[j] * dn[j] - sn * mean, ds[j]), gt = TOKEN ? g[j] * t : t;
+                o[j] = ra * (gt * wa[p][j] - on * mo);
+                s[j] = t * a.scale;
+                if (TOKEN) g[j] = t * on * wa[p][j];
+                sb[p][j] = fmaf(dn[j], sn, sb[p][j]);
+                sa[p][j] = fmaf(gt, on, sa[p][j]);
             }
             if (left(p) > 0) {
-                if (a.d_o.p) store8<DT>(a.d_o.p, r * a.d_o.ld + col(p), left(p), false, d_o);
-                if (a.dres.p) store8<DT>(a.dres.p, r * a.dres.ld + col(p), left(p), a.dres.f32, t);
-                if (a.dgate.p) store8<DT>(a.dgate.p, r * a.dgate.ld + col(p), left(p), false, u);
+                if (a.d_o.p) store8<DT>(a.d_o.p, r * a.d_o.ld + col(p), left(p), false, o);
+                if (a.dres.p) store8<DT>(a.dres.p, r * a.dres.ld + col(p), left(p), a.dres.f32, s);
+                if (TOKEN && a.dgate.p) store8<DT>(a.dgate.p, r * a.dgate.ld + col(p), left(p), false, g);
             }
         }
-        if (blockDim.x > 64) __syncthreads();       // part
     }
-    float *out = a.partial + (int64_t)blockIdx.x * 3 * a.H;
+    // the groups' sums, in order, through LDS
+    float *out = a.partial + (int64_t)blockIdx.x * 2 * a.H;
+    if (!a.dwa && !a.dwb && !a.dg) return;
+    for (int k = 0; k < 2; k++) {
+        if (groups > 1) {
+            __syncthreads();
 #pragma unroll
-    for (int p = 0; p < P; p++)
-        if (left(p) > 0) {
-            if (a.dwa) store8<DT>(out, col(p), left(p), true, da[p]);
-            if (a.dwb) store8<DT>(out, a.H + col(p), left(p), true, db[p]);
-            if (a.dg) store8<DT>(out, 2 * a.H + col(p), left(p), true, dg[p]);
+            for (int p = 0; p < P; p++)
+#pragma unroll
+                for (int j = 0; j < 8; j++) joined[(group * P * 8 + p * 8 + j) * nt + tid] = k ? sb[p][j] : sa[p][j];
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int p = 0; p < P; p++)
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        for (int i = 1; i < groups; i++) {
+                            const float v = joined[(i * P * 8 + p * 8 + j) * nt + tid];
+                            if (k) sb[p][j] += v;
+                            else sa[p][j] += v;
+                        }
+            }
         }
+        if (group == 0) {
+#pragma unroll
+            for (int p = 0; p < P; p++)
+                if (left(p) > 0) store8<DT>(out + k * a.H, col(p), left(p), true, k ? sb[p] : sa[p]);
+        }
+    }
 }
 
-// The slices' sums in order: 64 columns a block, four threads over the slices.
-__global__ void __launch_bounds__(256)
-k_norm_sums(const float *partial, int slices, int H, void *dwa, void *dwb, void *dg, int dw_dtype, int dg_dtype) {
-    __shared__ float red[4][64];
-    void *out = blockIdx.y == 0 ? dwa : blockIdx.y == 1 ? dwb : dg;
-    const int dtype = blockIdx.y == 2 ? dg_dtype : dw_dtype;
-    if (!out) return;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx;
+// The slices' sums: 64 columns a block, 16 threads over the slices, 4 loads of
+// each together; then dw_a = g sum, dg = w_a sum (a gate by token: dw_a = sum).
+template <int DT>
+__global__ void __launch_bounds__(1024)
+k_norm_sums(NormBackArgs a, int slices, bool token) {
+    __shared__ float red[16][64];
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6, c = blockIdx.x * 64 + tx, k = blockIdx.y;
+    if (k ? !a.dwb : !a.dwa && !a.dg) return;
+    const float *p = a.partial + (int64_t)k * a.H + c;
+    const int64_t step = 2 * (int64_t)a.H;
     float s = 0.f;
-    if (c < H)
-        for (int i = ty; i < slices; i += 4) s += partial[((int64_t)i * 3 + blockIdx.y) * H + c];
+    if (c < a.H)
+        for (int i = ty; i < slices; i += 64) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[j] = i + 16 * j < slices ? p[(i + 16 * j) * step] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; j++) s += v[j];
+        }
     red[ty][tx] = s;
     __syncthreads();
-    if (ty || c >= H) return;
-    s = red[0][tx] + red[1][tx] + red[2][tx] + red[3][tx];
-    if (dtype == BITMOE_F32) static_cast<float *>(out)[c] = s;
-    else static_cast<uint16_t *>(out)[c] = (uint16_t)(dtype == BITMOE_BF16 ? elem_pair<BITMOE_BF16>(s, 0.f)
-                                                                          : elem_pair<BITMOE_F16>(s, 0.f));
+    if (ty || c >= a.H) return;
+#pragma unroll
+    for (int i = 1; i < 16; i++) s += red[i][tx];
+    auto put = [&](void *out, int dtype, float v) {
+        if (!out) return;
+        if (dtype == BITMOE_F32) static_cast<float *>(out)[c] = v;
+        else static_cast<uint16_t *>(out)[c] = (uint16_t)elem_pair<DT>(v, 0.f);
+    };
+    auto at = [&](const void *w) { return w ? elem_f32<DT>(static_cast<const uint16_t *>(w)[c]) : 1.f; };
+    if (k) {
+        put(a.dwb, a.dw_dtype, s);
+    } else {
+        put(a.dwa, a.dw_dtype, token ? s : s * at(a.gate.p));
+        put(a.dg, a.dg_dtype, s * at(a.wa));
+    }
 }
 
 // threads of a row, and pieces of each
@@ -258,26 +411,36 @@ int launch_block_norm(const NormArgs &args, int dtype, hipStream_t st) {
     });
 }
 
+// a workgroup a compute unit (two of 16 waves do not fit in the registers)
+static int row_groups(int H) { return 1024 / row_threads(H); }
 int norm_slices(int T, int H) {
-    (void)H;
-    return std::min(T, 512);
+    const int groups = row_groups(H);
+    return std::min((T + groups - 1) / groups, 256);
 }
 
-int launch_block_norm_backward(const NormBackArgs &a, int dtype, hipStream_t st) {
-    const int slices = norm_slices(a.T, a.H);
-    if (slices > 0) {
-        const int rc = with(dtype, a.H, [&](auto dt, auto p) {
-            k_block_norm_backward<dt.value, p.value><<<slices, row_threads(a.H), 0, st>>>(a);
+int launch_block_norm_backward(const NormBackArgs &args, int dtype, hipStream_t st) {
+    NormBackArgs a = args;
+    const int slices = norm_slices(a.T, a.H), nt = row_threads(a.H), groups = row_groups(a.H);
+    const bool token = a.gate.p && a.gate.ld != 0, wide = a.s.f32 || a.ds.f32;
+    return with(dtype, a.H, [&](auto dt, auto p) {
+        constexpr int DT = dt.value, P = p.value;
+        if (slices > 0) {
+            auto go = [&](auto w, auto t) {
+                const size_t lds = groups > 1 ? (size_t)groups * nt * P * 8 * 4 : 0;
+                k_block_norm_backward<DT, P, decltype(w)::value, decltype(t)::value><<<slices, nt * groups, lds, st>>>(a, nt, groups);
+            };
+            if (wide && token) go(std::true_type{}, std::true_type{});
+            else if (wide) go(std::true_type{}, std::false_type{});
+            else if (token) go(std::false_type{}, std::true_type{});
+            else go(std::false_type{}, std::false_type{});
             BM_LAUNCH_CHECK();
-            return BITMOE_OK;
-        });
-        if (rc) return rc;
-    }
-    if (a.dwa || a.dwb || a.dg) {
-        k_norm_sums<<<dim3((a.H + 63) / 64, 3), 256, 0, st>>>(a.partial, slices, a.H, a.dwa, a.dwb, a.dg, a.dw_dtype, a.dg_dtype);
-        BM_LAUNCH_CHECK();
-    }
-    return BITMOE_OK;
+        }
+        if (a.dwa || a.dwb || a.dg) {
+            k_norm_sums<DT><<<dim3((a.H + 63) / 64, 2), 1024, 0, st>>>(a, slices, token);
+            BM_LAUNCH_CHECK();
+        }
+        return BITMOE_OK;
+    });
 }
 
 }  // namespace bm_host

@@ -37,6 +37,13 @@ int launch_swiglu_checkpoint_backward(const bitmoe_rows &dh, const bitmoe_rows8 
 GemmPlan i8_plan(const GemmArgs &g, bool whole);
 bool i8_whole(const GemmArgs &g);            // every row begins on 16 bytes and has whole 16-byte pieces
 size_t i8_ws_bytes(int E, int R, int N, int K);
+// Operands laid on 16 bytes in the workspace: rows of `ld` codes (zeros behind K),
+// the call's rows of x at `x` with their scales at `scale`, the experts' at `w`.
+struct I8Pack {
+    int64_t ld;
+    size_t x, scale, w, bytes;
+};
+I8Pack i8_pack(int E, int R, int N, int K);
 int launch_gemm_i8(int out, const GemmArgs &g, void *ws, hipStream_t s);
 
 }  // namespace bm_host

@@ -87,11 +87,20 @@ def _experts8(q, what):
 
 
 def _new_rows8(rows, cols, block, dev):
-    torch = _torch()
+    """(a new Rows8, its bitmoe_rows8: nothing of it needs a check)"""
     if block not in BLOCKS:
         raise ValueError(f"block must be one of {BLOCKS}")
-    return Rows8(torch.empty((rows, cols), dtype=torch.int8, device=dev),
-                 torch.empty((rows, -(-cols // block)) if block else (rows,), dtype=torch.float32, device=dev), block)
+    torch = _torch()
+    codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    n = -(-cols // block) if block else 1
+    scale = torch.empty((rows, n) if block else (rows,), dtype=torch.float32, device=dev)
+    return Rows8(codes, scale, block), _ROWS8.pack(codes.data_ptr(), 0, cols, rows, cols, 1, I8, scale.data_ptr(), n, block, 0)
+
+
+def _given_rows8(out, shape, block):
+    if out.block != block:
+        raise ValueError("out is not of block")
+    return _rows8(out, "out", shape)
 
 
 def quantize_rows(x, block=0, out=None, stream=None):
@@ -113,10 +122,10 @@ def quantize_rows(x, block=0, out=None, stream=None):
         return Rows8(q.codes.view(E, N, K), q.scale.view(E, N), 0)
     xr = _rows(x, "x", f32=True)
     if out is None:
-        out = _new_rows8(*x.shape, block, dev)
-    elif out.block != block:
-        raise ValueError("out is not of block")
-    _check(lib().moe_quantize_rows(xr, _rows8(out, "out", x.shape), _current_stream(dev)), "moe_quantize_rows")
+        out, qr = _new_rows8(*x.shape, block, dev)
+    else:
+        qr = _given_rows8(out, x.shape, block)
+    _check(lib().moe_quantize_rows(xr, qr, _current_stream(dev)), "moe_quantize_rows")
     return out
 
 
@@ -198,18 +207,17 @@ def swiglu_rows8(gate, up, block=0, out=None, stream=None):
     g = _rows(gate, "gate")
     _one_type("gate and up", gate, up)
     if out is None:
-        out = _new_rows8(*gate.shape, block, dev)
-    elif out.block != block:
-        raise ValueError("out is not of block")
-    _check(lib().moe_swiglu_rows8(g, _rows(up, "up", gate.shape), _rows8(out, "out", gate.shape), _current_stream(dev)),
-           "moe_swiglu_rows8")
+        out, qr = _new_rows8(*gate.shape, block, dev)
+    else:
+        qr = _given_rows8(out, gate.shape, block)
+    _check(lib().moe_swiglu_rows8(g, _rows(up, "up", gate.shape), qr, _current_stream(dev)), "moe_swiglu_rows8")
     return out
 
 
 def swiglu_checkpoint(gate, up, block=64, h=None, gate8=None, up8=None, stream=None):
     """swiglu, and its inputs in 8 bits for swiglu_checkpoint_backward: (h, gate8,
-    up8), the last two Rows8 of `block` 32, 64 or 128 (halves of one new [R, 2 I]
-    matrix each of codes and of scales, if not given)."""
+    up8), the last two Rows8 of `block` 32, 64 or 128 (halves of one new tensor
+    of codes and one of scales, if not given)."""
     given = [t for q in (gate8, up8) if q is not None for t in (q.codes, q.scale)]
     dev = _device(gate, up, h, *given)
     there = _elsewhere(dev, stream)
@@ -226,12 +234,18 @@ def swiglu_checkpoint(gate, up, block=64, h=None, gate8=None, up8=None, stream=N
             raise ValueError(f"block must be one of {BLOCKS[1:]}")
         torch = _torch()
         n = -(-I // block)
-        codes = torch.empty((R, 2 * I), dtype=torch.int8, device=dev)
-        scale = torch.empty((R, 2 * n), dtype=torch.float32, device=dev)
-        gate8, up8 = Rows8(codes[:, :I], scale[:, :n], block), Rows8(codes[:, I:], scale[:, n:], block)
+        codes = torch.empty((2, R, I), dtype=torch.int8, device=dev)
+        scale = torch.empty((2, R, n), dtype=torch.float32, device=dev)
+        (gc, uc), (gs, us) = codes.unbind(0), scale.unbind(0)
+        gate8, up8 = Rows8(gc, gs, block), Rows8(uc, us, block)
+        at, sat = codes.data_ptr(), scale.data_ptr()
+        gr = _ROWS8.pack(at, 0, I, R, I, 1, I8, sat, n, block, 0)
+        ur = _ROWS8.pack(at + R * I, 0, I, R, I, 1, I8, sat + 4 * R * n, n, block, 0)
+    else:
+        gr, ur = _rows8(gate8, "gate8", shape), _rows8(up8, "up8", shape)
     h = _output(h, shape, gate.dtype, dev, "h")
-    _check(lib().moe_swiglu_checkpoint(g, _rows(up, "up", shape), _rows(h, "h", shape), _rows8(gate8, "gate8", shape),
-                                       _rows8(up8, "up8", shape), _current_stream(dev)), "moe_swiglu_checkpoint")
+    _check(lib().moe_swiglu_checkpoint(g, _rows(up, "up", shape), _rows(h, "h", shape), gr, ur, _current_stream(dev)),
+           "moe_swiglu_checkpoint")
     return h, gate8, up8
 
 
@@ -251,7 +265,7 @@ def swiglu_checkpoint_backward(dh, gate8, up8, dgate=None, dup=None, need_h=Fals
     shape = dh.shape
     if dgate is None:
         both = _torch().empty((shape[0], 2 * shape[1]), dtype=dh.dtype, device=dev)
-        dgate, dup = both[:, :shape[1]], both[:, shape[1]:]
+        dgate, dup = both.split(shape[1], 1) if shape[1] else (both, both)
     if h is None and need_h:
         h = _torch().empty(shape, dtype=dh.dtype, device=dev)
     _one_type("dh, dgate, dup and h", dh, dgate, dup, *(() if h is None else (h,)))
