@@ -172,8 +172,8 @@ BM_DEV void hold(uint4 &q) { asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), 
 // is it times g, dg it times w_a) and ends as one slice of the partial sums.  One
 // barrier a row: what it separates alternates between two places (three for
 // `far`, which also has to be cleared).
-template <int DT, int P, bool WIDE, bool TOKEN>
-__global__ void __launch_bounds__(1024)
+template <int DT, int P, int MOST, bool WIDE, bool TOKEN>
+__global__ void __launch_bounds__(MOST)
 k_block_norm_backward(NormBackArgs a, int nt, int groups) {
     __shared__ float part[3][kMost][8];
     __shared__ int far[3];
@@ -230,7 +230,8 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
 #pragma unroll
         for (int p = 0; p < P; p++) row[p] = ahead[p];
         load(r + step);
-        // (the row's values stay as they are in memory: half the registers, unpacked twice)
+        // (the row's values stay as they are in memory, half the registers, and are unpacked
+        // for each pass anew, which the compiler would not do by itself)
         float q[6], fs = 1.f, fo = 1.f;
         auto sums = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -255,6 +256,22 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
                     q[4] = fmaf(u, d, q[4]);
                     q[5] = fmaf(u, x, q[5]);
                 }
+                __builtin_amdgcn_sched_barrier(0);         // (one piece's values at a time in registers)
+            }
+        };
+        auto anew = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+                hold(row[p].dn.lo);
+                hold(row[p].o.lo);
+                hold(row[p].s.lo);
+                hold(row[p].ds.lo);
+                if (WIDE) hold(row[p].s.hi);
+                if (WIDE) hold(row[p].ds.hi);
+                if (TOKEN) hold(row[p].g.lo);
+                hold(wb[p]);
+#pragma unroll
+                for (int j = 0; j < 8; j++) asm volatile("" : "+v"(wa[p][j]));
             }
         };
         sums();
@@ -268,6 +285,7 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
         if (far[three]) {
             fs = q[0] < 0x1p120f ? 1.f : kDown;
             fo = q[2] < 0x1p120f ? 1.f : kDown;
+            anew();
             sums();
             put_sums<6>(q, part[2], wave);
             __syncthreads();
@@ -281,16 +299,7 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
         const float b = a.dn.p ? fs * b1 : 0.f, mean = b1 * q[1] / (float)a.H;             // of p and s b
         const float vo = q[3] + b * (q[4] - b1 * mean * q[5]), ra = fo * a1, mo = a1 * vo / (float)a.H;
         if (r >= a.T) continue;
-        // (unpacked anew, which the compiler would not do by itself)
-#pragma unroll
-        for (int p = 0; p < P; p++) {
-            hold(row[p].dn.lo);
-            hold(row[p].o.lo);
-            hold(row[p].s.lo);
-            hold(row[p].ds.lo);
-            if (TOKEN) hold(row[p].g.lo);
-            hold(wb[p]);
-        }
+        anew();
 #pragma unroll
         for (int p = 0; p < P; p++) {
             float dn[8], ds[8], s[8], o[8], g[8], w[8];
@@ -316,6 +325,7 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
                 if (a.dres.p) store8<DT>(a.dres.p, r * a.dres.ld + col(p), left(p), a.dres.f32, s);
                 if (TOKEN && a.dgate.p) store8<DT>(a.dgate.p, r * a.dgate.ld + col(p), left(p), false, g);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     // the groups' sums, in order, through LDS
@@ -411,23 +421,37 @@ int launch_block_norm(const NormArgs &args, int dtype, hipStream_t st) {
     });
 }
 
-// a workgroup a compute unit (two of 16 waves do not fit in the registers)
-static int row_groups(int H) { return 1024 / row_threads(H); }
+// The backward pass's threads of a row and rows of a workgroup: 8 columns a thread up
+// to 2048, 16 above, in workgroups of 4 waves, or as many as a row needs; `slices`
+// of them run at a time (3, 2, 1 on a compute unit, by their registers).
+struct BackShape {
+    int pieces, nt, groups, slices;
+};
+static BackShape back_shape(int H) {
+    BackShape b{H <= 2048 ? 1 : 2, 0, 1, H <= 2048 ? 768 : H <= 4096 ? 512 : 256};
+    b.nt = (H + b.pieces * 512 - 1) / (b.pieces * 512) * 64;
+    b.groups = std::max(256 / b.nt, 1);
+    return b;
+}
 int norm_slices(int T, int H) {
-    const int groups = row_groups(H);
-    return std::min((T + groups - 1) / groups, 256);
+    const BackShape b = back_shape(H);
+    return std::min((T + b.groups - 1) / b.groups, b.slices);
 }
 
 int launch_block_norm_backward(const NormBackArgs &args, int dtype, hipStream_t st) {
     NormBackArgs a = args;
-    const int slices = norm_slices(a.T, a.H), nt = row_threads(a.H), groups = row_groups(a.H);
+    const BackShape b = back_shape(a.H);
+    const int slices = norm_slices(a.T, a.H);
     const bool token = a.gate.p && a.gate.ld != 0, wide = a.s.f32 || a.ds.f32;
-    return with(dtype, a.H, [&](auto dt, auto p) {
-        constexpr int DT = dt.value, P = p.value;
+    auto of = [&](auto dt) {
+        constexpr int DT = dt.value;
         if (slices > 0) {
+            const size_t lds = b.groups > 1 ? (size_t)b.groups * b.nt * b.pieces * 8 * 4 : 0;
             auto go = [&](auto w, auto t) {
-                const size_t lds = groups > 1 ? (size_t)groups * nt * P * 8 * 4 : 0;
-                k_block_norm_backward<DT, P, decltype(w)::value, decltype(t)::value><<<slices, nt * groups, lds, st>>>(a, nt, groups);
+                constexpr bool W = decltype(w)::value, K = decltype(t)::value;
+                if (b.pieces == 1) k_block_norm_backward<DT, 1, 256, W, K><<<slices, b.nt * b.groups, lds, st>>>(a, b.nt, b.groups);
+                else if (b.nt <= 512) k_block_norm_backward<DT, 2, 512, W, K><<<slices, b.nt * b.groups, lds, st>>>(a, b.nt, b.groups);
+                else k_block_norm_backward<DT, 2, 1024, W, K><<<slices, b.nt * b.groups, lds, st>>>(a, b.nt, b.groups);
             };
             if (wide && token) go(std::true_type{}, std::true_type{});
             else if (wide) go(std::true_type{}, std::false_type{});
@@ -440,7 +464,8 @@ int launch_block_norm_backward(const NormBackArgs &args, int dtype, hipStream_t 
             BM_LAUNCH_CHECK();
         }
         return BITMOE_OK;
-    });
+    };
+    return dtype == BITMOE_BF16 ? of(std::integral_constant<int, BITMOE_BF16>{}) : of(std::integral_constant<int, BITMOE_F16>{});
 }
 
 }  // namespace bm_host
