@@ -66,7 +66,7 @@ int moe_block_norm(const bitmoe_rows *o, const void *w_after, const bitmoe_rows 
 
 size_t moe_block_norm_backward_workspace_bytes(int T, int H) {
     if (check_sizes(1, T, H, 1) || H > kMaxNormCols) return 0;
-    return up256((size_t)norm_slices(T, H) * 2 * H * 4);
+    return up256((size_t)norm_shape(T, H).slices * 2 * H * 4);
 }
 
 int moe_block_norm_backward(const bitmoe_rows *dn, const bitmoe_rows *ds, const bitmoe_rows *s, const bitmoe_rows *o,

@@ -1,5 +1,5 @@
 // Host-side interface of the norms around a block: the arguments that the C
-// ABI's checks (norm.cpp) hand to the launchers in norm_kernels.hip.
+// ABI's checks (norm.cpp) hand to the launchers in norm_bf16.hip and norm_f16.hip.
 #pragma once
 
 #include "experts_check.h"
@@ -34,7 +34,25 @@ struct NormBackArgs {
     int32_t dw_dtype, dg_dtype;
     float *partial;                         // [slices][2][H]
 };
-int norm_slices(int T, int H);
 int launch_block_norm_backward(const NormBackArgs &a, int dtype, hipStream_t st);
+int launch_block_norm_f16(const NormArgs &a, hipStream_t st);
+int launch_block_norm_backward_f16(const NormBackArgs &a, hipStream_t st);
+
+// The backward pass's launch: pieces of 8 columns a thread, threads of a row, rows
+// of a workgroup, and workgroups, each of which leaves a slice of partial sums.  8
+// columns a thread up to 2048, 16 above, in workgroups of 4 waves, or as many as a row
+// needs; so many of them as run at a time (3, 2, 1 on a compute unit, by their
+// registers).
+struct NormShape {
+    int pieces, nt, groups, slices;
+};
+inline NormShape norm_shape(int T, int H) {
+    NormShape b{H <= 2048 ? 1 : 2, 0, 1, 0};
+    b.nt = (H + b.pieces * 512 - 1) / (b.pieces * 512) * 64;
+    b.groups = b.nt <= 128 ? 256 / b.nt : 1;
+    const int most = H <= 2048 ? 768 : H <= 4096 ? 512 : 256, need = (T + b.groups - 1) / b.groups;
+    b.slices = need < most ? need : most;
+    return b;
+}
 
 }  // namespace bm_host

@@ -3,16 +3,19 @@
 // and their gradients.  With p = w_b dn, t = ds + b (p - s b^2 <p, s> / H) and
 // v = g t w_a:  dr = scale t,  do = a (v - o a^2 <v, o> / H),
 //   dw_a = sum t g o a,  dg = t o a w_a,  dw_b = sum dn s b.
-// A row is taken by as many threads as it has 8 columns (16 where it is wider
-// than 8192), and stays in their registers from the sums to the outputs.  The
+// A row is taken by a workgroup's threads (or several rows by a part of them each),
+// 8 columns a piece, and stays in their registers from the sums to the outputs.  The
 // backward pass needs all its sums in one step: <v, o> is taken apart into
 // <g w_a o, ds>, <g w_a o, p> and <g w_a o, s>, which do not need t.
+#pragma once
+
+#include <initializer_list>
+
 #include "norm.h"
 #include "rows_util.h"
 
-namespace {
+namespace bm {
 
-using namespace bm;
 using bm_host::NormArgs;
 using bm_host::NormBackArgs;
 using bm_host::NormMat;
@@ -54,19 +57,22 @@ BM_DEV void get_sums(float (&v)[N], const float (*part)[8], int nw) {
 constexpr float kDown = 0x1p-80f;   // f where the squares' sum leaves fp32
 BM_DEV float inv_rms(float sum, int H, float eps, float f) { return rsqrtf(sum / (float)H + eps * f * f); }
 
-template <int DT>
-BM_DEV void load_w(const void *w, int c, int n, float (&v)[8]) {
-    if (w) load8<DT>(w, c, n, false, v);
-    else
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = 1.f;
-}
-template <int DT>
-BM_DEV void load_m(const NormMat &m, int64_t r, int c, int n, float missing, float (&v)[8]) {
-    if (m.p) load8<DT>(m.p, r * m.ld + c, n, m.f32, v);
+// the first n (<= 0: none) of eight columns from c of row r, `missing` for a matrix
+// that is not there
+template <int DT, int PAST>
+BM_DEV void load_cols(const NormMat &m, int64_t r, int c, int n, float missing, float (&v)[8]) {
+    if (m.p) load_values<DT, PAST>(m.p, r * m.ld + c, n, m.f32, v);
     else
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = missing;
+}
+template <int DT>
+BM_DEV void load_w(const void *w, int c, int n, float (&v)[8]) {
+    load_cols<DT, kCached>(NormMat{const_cast<void *>(w), 0, false}, 0, c, n, 1.f, v);
+}
+template <int DT, int PAST>
+BM_DEV void store_cols(const NormMat &m, int64_t r, int c, int n, const float (&v)[8]) {
+    store_values<DT, PAST>(m.p, r * m.ld + c, n, m.f32, v);
 }
 
 template <int DT, int P>
@@ -74,15 +80,13 @@ __global__ void __launch_bounds__(1024)
 k_block_norm(NormArgs a) {
     __shared__ float part[4][kMost][8];
     const int64_t r = blockIdx.x;
-    const int step = blockDim.x * 8;
     float v[P][8], o[P][8];
-    auto col = [&](int p) { return (int)threadIdx.x * 8 + p * step; };
-    auto left = [&](int p) { return min(max(a.H - col(p), 0), 8); };
-    auto at = [&](int p) { return min(col(p), a.H - 1); };          // (an address inside the row, of which `left` are read)
+    auto col = [&](int p) { return (int)(threadIdx.x + p * blockDim.x) * 8; };
+    auto left = [&](int p) { return a.H - col(p); };
 #pragma unroll
     for (int p = 0; p < P; p++) {
-        load_m<DT>(a.o, r, at(p), left(p), 0.f, o[p]);
-        load_m<DT>(a.res, r, at(p), left(p), 0.f, v[p]);
+        load_cols<DT, kCached>(a.o, r, col(p), left(p), 0.f, o[p]);
+        load_cols<DT, kCached>(a.res, r, col(p), left(p), 0.f, v[p]);
     }
     auto squares = [&](const float (&x)[P][8], float f, int k) {
         float s[1] = {0.f};
@@ -106,8 +110,8 @@ k_block_norm(NormArgs a) {
 #pragma unroll
         for (int p = 0; p < P; p++) {
             float w[8], g[8];
-            load_w<DT>(a.wa, at(p), left(p), w);
-            load_m<DT>(a.gate, r, at(p), left(p), 1.f, g);
+            load_w<DT>(a.wa, col(p), left(p), w);
+            load_cols<DT, kCached>(a.gate, r, col(p), left(p), 1.f, g);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[p][j] = fmaf(g[j], o[p][j] * f * ra * w[j], v[p][j]);
         }
@@ -115,7 +119,7 @@ k_block_norm(NormArgs a) {
     if (a.s.p) {
 #pragma unroll
         for (int p = 0; p < P; p++)
-            if (left(p) > 0) store8<DT>(a.s.p, r * a.s.ld + col(p), left(p), a.s.f32, v[p]);
+            if (left(p) > 0) store_cols<DT, kCached>(a.s, r, col(p), left(p), v[p]);
     }
     if (!a.n.p) return;
     float f = 1.f, sum = squares(v, f, 2);
@@ -124,10 +128,10 @@ k_block_norm(NormArgs a) {
 #pragma unroll
     for (int p = 0; p < P; p++) {
         float w[8];
-        load_w<DT>(a.wb, at(p), left(p), w);
+        load_w<DT>(a.wb, col(p), left(p), w);
 #pragma unroll
         for (int j = 0; j < 8; j++) v[p][j] = v[p][j] * f * rb * w[j];
-        if (left(p) > 0) store8<DT>(a.n.p, r * a.n.ld + col(p), left(p), false, v[p]);
+        if (left(p) > 0) store_cols<DT, kCached>(a.n, r, col(p), left(p), v[p]);
     }
 }
 
@@ -137,19 +141,19 @@ template <bool WIDE>
 struct Piece {
     uint4 lo, hi;
 };
-template <int DT, bool WIDE>
+template <int DT, int PAST, bool WIDE>
 BM_DEV void fetch(const NormMat &m, int64_t r, int c, int n, Piece<WIDE> &q) {
     q.lo = make_uint4(0, 0, 0, 0);
     if (WIDE) q.hi = make_uint4(0, 0, 0, 0);
     if (!m.p || n <= 0) return;
     if (WIDE && m.f32) {
         float v[8];
-        load8<DT>(m.p, r * m.ld + c, n, true, v);
+        load_values<DT, PAST>(m.p, r * m.ld + c, n, true, v);
         q.lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
         q.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     } else {
-        const uint16_t *p = static_cast<const uint16_t *>(m.p) + r * m.ld + c;
-        q.lo = n >= 8 ? load16(p) : load16_part(p, n);
+        const Mat t{m.p, m.ld};
+        q.lo = n >= 8 ? piece<true, PAST>(t, r, c, 0) : piece<false, PAST>(t, r, c, c + n);
     }
 }
 template <int DT, bool WIDE>
@@ -172,7 +176,7 @@ BM_DEV void hold(uint4 &q) { asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), 
 // is it times g, dg it times w_a) and ends as one slice of the partial sums.  One
 // barrier a row: what it separates alternates between two places (three for
 // `far`, which also has to be cleared).
-template <int DT, int P, int MOST, bool WIDE, bool TOKEN>
+template <int DT, int P, int MOST, int PAST, bool WIDE, bool TOKEN>
 __global__ void __launch_bounds__(MOST)
 k_block_norm_backward(NormBackArgs a, int nt, int groups) {
     __shared__ float part[3][kMost][8];
@@ -181,21 +185,21 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
     const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / nt), tid = threadIdx.x - group * nt;   // (nt: whole waves)
     const int nw = nt >> 6, wave = threadIdx.x >> 6, first = group * nw;
     auto col = [&](int p) { return (tid + p * nt) * 8; };
-    auto left = [&](int p) { return min(a.H - col(p), 8); };
+    auto left = [&](int p) { return a.H - col(p); };
     // g w_a (w_a alone for a gate by token); w_b stays as it is in memory
     float wa[P][8], sa[P][8], sb[P][8];
     uint4 wb[P];
 #pragma unroll
     for (int p = 0; p < P; p++) {
-        const int c = min(col(p), a.H - 1), n = max(left(p), 0);
         float g[8];
-        load_w<DT>(a.wa, c, n, wa[p]);
-        load_w<DT>(TOKEN ? nullptr : a.gate.p, c, n, g);
+        load_w<DT>(a.wa, col(p), left(p), wa[p]);
+        load_w<DT>(TOKEN ? nullptr : a.gate.p, col(p), left(p), g);
         const uint32_t one = elem_pair<DT>(1.f, 1.f);
         wb[p] = make_uint4(one, one, one, one);
         if (a.wb) {
-            const uint16_t *w = static_cast<const uint16_t *>(a.wb) + c;
-            wb[p] = n >= 8 ? load16(w) : load16_part(w, n);
+            Piece<false> w;
+            fetch<DT, kCached>(NormMat{const_cast<void *>(a.wb), 0, false}, 0, col(p), left(p), w);
+            wb[p] = w.lo;
         }
 #pragma unroll
         for (int j = 0; j < 8; j++) {
@@ -215,11 +219,11 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
 #pragma unroll
         for (int p = 0; p < P; p++) {
             const int n = r < a.T ? left(p) : 0;
-            fetch<DT>(a.dn, r, col(p), n, ahead[p].dn);
-            fetch<DT>(a.o, r, col(p), n, ahead[p].o);
-            fetch<DT>(a.s, r, col(p), n, ahead[p].s);
-            fetch<DT>(a.ds, r, col(p), n, ahead[p].ds);
-            if (TOKEN) fetch<DT>(a.gate, r, col(p), n, ahead[p].g);
+            fetch<DT, PAST>(a.dn, r, col(p), n, ahead[p].dn);
+            fetch<DT, PAST>(a.o, r, col(p), n, ahead[p].o);
+            fetch<DT, PAST>(a.s, r, col(p), n, ahead[p].s);
+            fetch<DT, PAST>(a.ds, r, col(p), n, ahead[p].ds);
+            if (TOKEN) fetch<DT, PAST>(a.gate, r, col(p), n, ahead[p].g);
         }
     };
     load((int64_t)blockIdx.x * groups + group);
@@ -321,16 +325,16 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
                 sa[p][j] = fmaf(gt, on, sa[p][j]);
             }
             if (left(p) > 0) {
-                if (a.d_o.p) store8<DT>(a.d_o.p, r * a.d_o.ld + col(p), left(p), false, o);
-                if (a.dres.p) store8<DT>(a.dres.p, r * a.dres.ld + col(p), left(p), a.dres.f32, s);
-                if (TOKEN && a.dgate.p) store8<DT>(a.dgate.p, r * a.dgate.ld + col(p), left(p), false, g);
+                if (a.d_o.p) store_cols<DT, PAST>(a.d_o, r, col(p), left(p), o);
+                if (a.dres.p) store_cols<DT, PAST>(a.dres, r, col(p), left(p), s);
+                if (TOKEN && a.dgate.p) store_cols<DT, PAST>(a.dgate, r, col(p), left(p), g);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     }
     // the groups' sums, in order, through LDS
-    float *out = a.partial + (int64_t)blockIdx.x * 2 * a.H;
     if (!a.dwa && !a.dwb && !a.dg) return;
+    const NormMat out{a.partial + (int64_t)blockIdx.x * 2 * a.H, a.H, true};
     for (int k = 0; k < 2; k++) {
         if (groups > 1) {
             __syncthreads();
@@ -354,7 +358,7 @@ k_block_norm_backward(NormBackArgs a, int nt, int groups) {
         if (group == 0) {
 #pragma unroll
             for (int p = 0; p < P; p++)
-                if (left(p) > 0) store8<DT>(out + k * a.H, col(p), left(p), true, k ? sb[p] : sa[p]);
+                if (left(p) > 0) store_cols<DT, kCached>(out, k, col(p), left(p), k ? sb[p] : sa[p]);
         }
     }
 }
@@ -397,75 +401,49 @@ k_norm_sums(NormBackArgs a, int slices, bool token) {
     }
 }
 
-// threads of a row, and pieces of each
-int row_threads(int H) { return std::min(((H + 7) / 8 + 63) / 64 * 64, 1024); }
-template <class F>
-int with(int dtype, int H, F f) {
-    auto typed = [&](auto dt) {
-        if (H <= 8192) return f(dt, std::integral_constant<int, 1>{});
-        return f(dt, std::integral_constant<int, 2>{});
-    };
-    return dtype == BITMOE_BF16 ? typed(std::integral_constant<int, BITMOE_BF16>{})
-                                : typed(std::integral_constant<int, BITMOE_F16>{});
+inline int64_t norm_bytes(int T, int H, std::initializer_list<const NormMat *> mats) {
+    int64_t n = 0;
+    for (const NormMat *m : mats)
+        if (m->p && m->ld) n += (int64_t)T * H * (m->f32 ? 4 : 2);
+    return n;
 }
 
-}  // namespace
-
-namespace bm_host {
-
-int launch_block_norm(const NormArgs &args, int dtype, hipStream_t st) {
-    return with(dtype, args.H, [&](auto dt, auto p) {
-        k_block_norm<dt.value, p.value><<<args.T, row_threads(args.H), 0, st>>>(args);
-        BM_LAUNCH_CHECK();
-        return BITMOE_OK;
-    });
+template <int DT>
+int launch_norm(const NormArgs &a, hipStream_t st) {
+    const int pieces = a.H <= 8192 ? 1 : 2, threads = (a.H + pieces * 512 - 1) / (pieces * 512) * 64;
+    if (pieces == 1) k_block_norm<DT, 1><<<a.T, threads, 0, st>>>(a);
+    else k_block_norm<DT, 2><<<a.T, threads, 0, st>>>(a);
+    BM_LAUNCH_CHECK();
+    return BITMOE_OK;
 }
 
-// The backward pass's threads of a row and rows of a workgroup: 8 columns a thread up
-// to 2048, 16 above, in workgroups of 4 waves, or as many as a row needs; `slices`
-// of them run at a time (3, 2, 1 on a compute unit, by their registers).
-struct BackShape {
-    int pieces, nt, groups, slices;
-};
-static BackShape back_shape(int H) {
-    BackShape b{H <= 2048 ? 1 : 2, 0, 1, H <= 2048 ? 768 : H <= 4096 ? 512 : 256};
-    b.nt = (H + b.pieces * 512 - 1) / (b.pieces * 512) * 64;
-    b.groups = std::max(256 / b.nt, 1);
-    return b;
-}
-int norm_slices(int T, int H) {
-    const BackShape b = back_shape(H);
-    return std::min((T + b.groups - 1) / b.groups, b.slices);
-}
-
-int launch_block_norm_backward(const NormBackArgs &args, int dtype, hipStream_t st) {
-    NormBackArgs a = args;
-    const BackShape b = back_shape(a.H);
-    const int slices = norm_slices(a.T, a.H);
+template <int DT>
+int launch_norm_backward(const NormBackArgs &a, hipStream_t st) {
+    const bm_host::NormShape b = bm_host::norm_shape(a.T, a.H);
     const bool token = a.gate.p && a.gate.ld != 0, wide = a.s.f32 || a.ds.f32;
-    auto of = [&](auto dt) {
-        constexpr int DT = dt.value;
-        if (slices > 0) {
-            const size_t lds = b.groups > 1 ? (size_t)b.groups * b.nt * b.pieces * 8 * 4 : 0;
-            auto go = [&](auto w, auto t) {
-                constexpr bool W = decltype(w)::value, K = decltype(t)::value;
-                if (b.pieces == 1) k_block_norm_backward<DT, 1, 256, W, K><<<slices, b.nt * b.groups, lds, st>>>(a, b.nt, b.groups);
-                else if (b.nt <= 512) k_block_norm_backward<DT, 2, 512, W, K><<<slices, b.nt * b.groups, lds, st>>>(a, b.nt, b.groups);
-                else k_block_norm_backward<DT, 2, 1024, W, K><<<slices, b.nt * b.groups, lds, st>>>(a, b.nt, b.groups);
-            };
-            if (wide && token) go(std::true_type{}, std::true_type{});
-            else if (wide) go(std::true_type{}, std::false_type{});
-            else if (token) go(std::false_type{}, std::true_type{});
-            else go(std::false_type{}, std::false_type{});
-            BM_LAUNCH_CHECK();
-        }
-        if (a.dwa || a.dwb || a.dg) {
-            k_norm_sums<DT><<<dim3((a.H + 63) / 64, 2), 1024, 0, st>>>(a, slices, token);
-            BM_LAUNCH_CHECK();
-        }
-        return BITMOE_OK;
-    };
-    return dtype == BITMOE_BF16 ? of(std::integral_constant<int, BITMOE_BF16>{}) : of(std::integral_constant<int, BITMOE_F16>{});
+    const bool past = past_cache(norm_bytes(a.T, a.H, {&a.dn, &a.ds, &a.s, &a.o, &a.gate, &a.d_o, &a.dres, &a.dgate})) != kCached;
+    if (b.slices > 0) {
+        const size_t lds = b.groups > 1 ? (size_t)b.groups * b.nt * b.pieces * 8 * 4 : 0;
+        auto go = [&](auto w, auto t, auto c) {
+            constexpr bool W = decltype(w)::value, K = decltype(t)::value;
+            constexpr int A = decltype(c)::value ? kLoadsPast : kCached;
+            const int n = b.nt * b.groups;
+            if (b.pieces == 1) k_block_norm_backward<DT, 1, 256, A, W, K><<<b.slices, n, lds, st>>>(a, b.nt, b.groups);
+            else if (b.nt <= 512) k_block_norm_backward<DT, 2, 512, A, W, K><<<b.slices, n, lds, st>>>(a, b.nt, b.groups);
+            else k_block_norm_backward<DT, 2, 1024, kCached, W, K><<<b.slices, n, lds, st>>>(a, b.nt, b.groups);
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        auto go2 = [&](auto w, auto t) { past ? go(w, t, yes) : go(w, t, no); };
+        if (wide) token ? go2(yes, yes) : go2(yes, no);
+        else token ? go2(no, yes) : go2(no, no);
+        BM_LAUNCH_CHECK();
+    }
+    if (a.dwa || a.dwb || a.dg) {
+        k_norm_sums<DT><<<dim3((a.H + 63) / 64, 2), 1024, 0, st>>>(a, b.slices, token);
+        BM_LAUNCH_CHECK();
+    }
+    return BITMOE_OK;
 }
 
-}  // namespace bm_host
+}  // namespace bm

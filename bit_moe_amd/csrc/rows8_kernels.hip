@@ -3,12 +3,14 @@
 // them, and with its inputs kept in them.
 //
 // A code is rint(127 x / m) for the block's largest magnitude m.  The quotient
-// has to be the correctly rounded one, because a tie (x = m / 2 gives 63.5) is
-// exact and common in 16 bits: an estimate t (1 / m), which may be an ulp off,
-// and one step on its exact remainder (an fma) give it for two more operations
-// than the estimate (q' = q + (t - q m) / m with 1 / m correctly rounded).  m and
-// x are first taken to m's own power of two, so nothing overflows on the way.
-// Every kernel is bound by memory.
+// t / m has to be right where it is a tie (x = m / 2 gives 63.5, which is common in
+// 16 bits) and within a few steps elsewhere, where no 16-bit x comes near one.  An
+// estimate q = t inv with inv = 1 / m to a step, and one move by its exact remainder
+// (an fma), q + (t - q m) inv, is: the move's own error is 2^-22 of two steps, so a
+// quotient that float32 holds comes out as it is.  m and x are first taken to m's own
+// power of two, so nothing overflows on the way.
+// Bound by memory, and close behind it by the arithmetic of a code (9 operations) and
+// of silu.
 #include "rows8.h"
 #include "rows_util.h"
 
@@ -29,10 +31,13 @@ BM_DEV Coder coder(uint32_t bits, float *scale) {
     const float m = __uint_as_float(bits);
     k.m = m * to1;
     k.f = 127.f * to1;
-    k.inv = 1.f / k.m;
+    k.inv = __builtin_amdgcn_rcpf(k.m);
     k.keep = bits != 0 && bits < 0x7F800000u ? 0xFFFFFFFFu : 0u;
-    // (at most what 127 times stays finite: fp32's largest value / 127, rounded down)
-    *scale = bits < 0x7F800000u ? fminf(m / 127.f, 0x1.0204060000000p+121f) : __uint_as_float(0x7FC00000u);
+    // m / 127, correctly rounded: an estimate by 1 / 127 rounded, and its remainder;
+    // at most what 127 times stays finite (fp32's largest value / 127, rounded down)
+    const float c = 1.f / 127.f, q = k.m * c, s = fmaf(fmaf(-127.f, q, k.m), c, q);
+    const float from1 = __uint_as_float((254u << 23) - __float_as_uint(to1));
+    *scale = bits < 0x7F800000u ? fminf(s * from1, 0x1.0204060000000p+121f) : __uint_as_float(0x7FC00000u);
     return k;
 }
 BM_DEV uint32_t max_bits(uint32_t m, float v) { return max(m, __float_as_uint(v) & 0x7FFFFFFFu); }
@@ -53,38 +58,47 @@ BM_DEV void value4(uint32_t w, float scale, float *v) {
     for (int j = 0; j < 4; j++) v[j] = ((float)(w >> (8 * j) & 0xFFu) - 128.f) * scale;
 }
 
-struct __attribute__((packed, aligned(1))) B64 { uint32_t w[2]; };
-struct __attribute__((packed, aligned(1))) B128 { uint32_t w[4]; };
-// the first n (1 .. 4 W) codes of W words
-template <int W>
-BM_DEV void put_codes(int8_t *p, int n, const uint32_t (&w)[W]) {
-    if (n >= 4 * W) {
-        typename std::conditional<W == 4, B128, B64>::type u;
-#pragma unroll
-        for (int j = 0; j < W; j++) u.w[j] = w[j];
-        *reinterpret_cast<decltype(u) *>(p) = u;
+typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));
+// the first n of eight codes
+BM_DEV void put_codes(int8_t *p, int n, const uint32_t (&w)[2]) {
+    if (n >= 8) {
+        *reinterpret_cast<u32x2_b *>(p) = u32x2_b{w[0], w[1]};
     } else {
 #pragma unroll
-        for (int j = 0; j < 4 * W; j++)
+        for (int j = 0; j < 8; j++)
             if (j < n) p[j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
     }
 }
-BM_DEV uint4 get_codes16(const int8_t *p, int n) {
-    if (n >= 16) {
-        const B128 u = *reinterpret_cast<const B128 *>(p);
-        return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+template <int PAST>
+BM_DEV uint2 get_codes(const int8_t *p, int n) {
+    if (n >= 8) {
+        const u32x2_b *q = reinterpret_cast<const u32x2_b *>(p);
+        const u32x2_b u = PAST == kCached ? *q : __builtin_nontemporal_load(q);
+        return make_uint2(u[0], u[1]);
     }
-    uint32_t w[4] = {0, 0, 0, 0};
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 16; j++)
+    for (int j = 0; j < 8; j++)
         if (j < n) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint2(w[0], w[1]);
 }
-BM_DEV void values16(const uint4 &u, float scale, float (&v)[16]) {
+BM_DEV void values8(const uint2 &u, float scale, float (&v)[8]) {
     value4(u.x, scale, v);
     value4(u.y, scale, v + 4);
-    value4(u.z, scale, v + 8);
-    value4(u.w, scale, v + 12);
+}
+
+// p = 1 / (1 + e^-z) and 1 - p, each to a few steps of its own: by t = e^-|z|, so that
+// the reciprocal is of 1 .. 2, where the one instruction is good to a step (a
+// division's ten, of values that a kernel needs once each, would bound these kernels)
+BM_DEV void logistic(float z, float *p, float *not_p) {
+    const float t = __expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.f + t), s = t * r;
+    *p = z < 0.f ? s : r;
+    *not_p = z < 0.f ? r : s;
+}
+BM_DEV float silu_of(float z) {
+    float p, q;
+    logistic(z, &p, &q);
+    return z * p;
 }
 
 struct Rows8 {
@@ -95,145 +109,139 @@ struct Rows8 {
 };
 
 // ---- blocks of columns ----------------------------------------------------
-// A thread takes 16 columns; the 2, 4 or 8 lanes of a block exchange their
-// largest magnitudes (all of them are there: a row's threads are a multiple of 8).
-template <int DT, bool F32>
-BM_DEV void load16v(const Mat &m, int64_t r, int c, int n, float (&v)[16]) {
-    load8<DT>(m.p, r * m.ld + c, n, F32, v);
-    load8<DT>(m.p, r * m.ld + c + 8, n - 8, F32, v + 8);
-}
-template <int DT>
-BM_DEV void store16v(const Mat &m, int64_t r, int c, int n, bool f32, const float (&v)[16]) {
-    store8<DT>(m.p, r * m.ld + c, n, f32, v);
-    if (n > 8) store8<DT>(m.p, r * m.ld + c + 8, n - 8, f32, v + 8);
-}
+// A thread takes 8 columns, so that each access of a wave is one run of memory (of
+// 16 a thread, stores past the cache would be halves of lines); the 4, 8 or 16 lanes
+// of a block exchange their largest magnitudes (all of them are there: a row's
+// threads are a multiple of 16).
 template <int CTRL>
 BM_DEV uint32_t dpp_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
 }
 template <int SHIFT>
-BM_DEV uint32_t block_max(const float (&v)[16]) {
+BM_DEV uint32_t block_max(const float (&v)[8]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 16; j++) m = max_bits(m, v[j]);
-    m = dpp_max<0xB1>(m);                        // lane ^ 1
-    if (SHIFT >= 6) m = dpp_max<0x4E>(m);        // lane ^ 2
-    if (SHIFT >= 7) m = dpp_max<0x141>(m);       // the other four of eight
+    for (int j = 0; j < 8; j++) m = max_bits(m, v[j]);
+    m = dpp_max<0x4E>(dpp_max<0xB1>(m));         // lanes ^ 1, ^ 2
+    if (SHIFT >= 6) m = dpp_max<0x141>(m);       // the other four of eight
+    if (SHIFT >= 7) m = dpp_max<0x140>(m);       // the other eight of sixteen
     return m;
 }
 template <int SHIFT>
-BM_DEV void put_block(const Rows8 &q, int64_t r, int c, int n, const float (&v)[16]) {
+BM_DEV void put_block(const Rows8 &q, int64_t r, int c, int n, const float (&v)[8]) {
     float scale;
     const Coder k = coder(block_max<SHIFT>(v), &scale);
-    const uint32_t w[4] = {code4(k, v), code4(k, v + 4), code4(k, v + 8), code4(k, v + 12)};
+    const uint32_t w[2] = {code4(k, v), code4(k, v + 4)};
     if (n > 0) put_codes(q.q + r * q.ld + c, n, w);
     if ((c & ((1 << SHIFT) - 1)) == 0 && n > 0) q.scale[r * q.ld_scale + (c >> SHIFT)] = scale;
 }
-// body(row, column, how many of its 16 are there) for every thread of every
+// body(row, column, how many of its 8 are there) for every thread of every
 // block of columns that has any
 template <int SHIFT, class F>
 BM_DEV void for_blocks(int rows, int cols, int cshift, F body) {
-    const int c = ((blockIdx.x << cshift) + (threadIdx.x & ((1 << cshift) - 1))) * 16;
+    const int c = ((blockIdx.x << cshift) + (threadIdx.x & ((1 << cshift) - 1))) * 8;
     const int step = gridDim.y * (256 >> cshift);
     int r = blockIdx.y * (256 >> cshift) + (threadIdx.x >> cshift);
     const int first = c & ~((1 << SHIFT) - 1);
     if (first + (1 << SHIFT) <= cols) {
-        for (; r < rows; r += step) body(r, c, std::integral_constant<int, 16>{});
+        for (; r < rows; r += step) body(r, c, std::integral_constant<int, 8>{});
     } else if (first < cols) {
-        for (; r < rows; r += step) body(r, c, min(max(cols - c, 0), 16));
+        for (; r < rows; r += step) body(r, c, min(max(cols - c, 0), 8));
     }
 }
 
-template <int DT, bool F32, int SHIFT>
+template <int DT, bool F32, int SHIFT, int PAST>
 __global__ void __launch_bounds__(256)
 k_quantize_blocks(Mat x, Rows8 q, int R, int C, int cshift) {
     for_blocks<SHIFT>(R, C, cshift, [&](int r, int c, auto n) {
-        float v[16];
-        load16v<DT, F32>(x, r, c, n, v);
+        float v[8];
+        load_values<DT, PAST>(x.p, r * x.ld + c, n, F32, v);
         put_block<SHIFT>(q, r, c, n, v);
     });
 }
 
-template <int DT, int SHIFT>
+template <int DT, int SHIFT, int PAST>
 __global__ void __launch_bounds__(256)
 k_swiglu_blocks(Mat gate, Mat up, Rows8 q, int R, int I, int cshift) {
     for_blocks<SHIFT>(R, I, cshift, [&](int r, int c, auto n) {
-        float g[16], u[16];
-        load16v<DT, false>(gate, r, c, n, g);
-        load16v<DT, false>(up, r, c, n, u);
+        float g[8], u[8];
+        load_values<DT, PAST>(gate.p, r * gate.ld + c, n, false, g);
+        load_values<DT, PAST>(up.p, r * up.ld + c, n, false, u);
 #pragma unroll
-        for (int j = 0; j < 16; j++) g[j] = silu(g[j]) * u[j];
+        for (int j = 0; j < 8; j++) g[j] = silu_of(g[j]) * u[j];
         put_block<SHIFT>(q, r, c, n, g);
     });
 }
 
-template <int DT, int SHIFT>
+template <int DT, int SHIFT, int PAST>
 __global__ void __launch_bounds__(256)
 k_swiglu_checkpoint(Mat gate, Mat up, Mat h, Rows8 gate8, Rows8 up8, int R, int I, int cshift) {
     for_blocks<SHIFT>(R, I, cshift, [&](int r, int c, auto n) {
-        float g[16], u[16];
-        load16v<DT, false>(gate, r, c, n, g);
-        load16v<DT, false>(up, r, c, n, u);
+        float g[8], u[8];
+        load_values<DT, PAST>(gate.p, r * gate.ld + c, n, false, g);
+        load_values<DT, PAST>(up.p, r * up.ld + c, n, false, u);
         put_block<SHIFT>(gate8, r, c, n, g);
         put_block<SHIFT>(up8, r, c, n, u);
 #pragma unroll
-        for (int j = 0; j < 16; j++) g[j] = silu(g[j]) * u[j];
-        store16v<DT>(h, r, c, n, false, g);
+        for (int j = 0; j < 8; j++) g[j] = silu_of(g[j]) * u[j];
+        if (n > 0) store_values<DT, PAST>(h.p, r * h.ld + c, n, false, g);
     });
 }
 
-template <int DT>
+template <int DT, int PAST>
 __global__ void __launch_bounds__(256)
 k_swiglu_checkpoint_backward(Mat dh, Rows8 gate8, Rows8 up8, Mat dgate, Mat dup, Mat h, int R, int I, int cshift) {
-    for_blocks<4>(R, I, cshift, [&](int r, int c, auto n) {
-        float d[16], g[16], u[16];
-        const uint4 cg = get_codes16(gate8.q + r * gate8.ld + c, n), cu = get_codes16(up8.q + r * up8.ld + c, n);
+    for_blocks<3>(R, I, cshift, [&](int r, int c, auto n) {
+        float d[8], g[8], u[8];
+        const uint2 cg = get_codes<PAST>(gate8.q + r * gate8.ld + c, n), cu = get_codes<PAST>(up8.q + r * up8.ld + c, n);
         const float sg = gate8.scale[r * gate8.ld_scale + (c >> gate8.shift)];
         const float su = up8.scale[r * up8.ld_scale + (c >> up8.shift)];
-        load16v<DT, false>(dh, r, c, n, d);
-        values16(cg, sg, g);
-        values16(cu, su, u);
+        load_values<DT, PAST>(dh.p, r * dh.ld + c, n, false, d);
+        values8(cg, sg, g);
+        values8(cu, su, u);
         // with p = 1 / (1 + e^-gate): dgate = dh up p (1 + gate (1 - p)), dup = dh gate p, h = gate p up
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
-            const float p = 1.f / (1.f + __expf(-g[j])), v = g[j] * p;
-            g[j] = d[j] * u[j] * p * (1.f + g[j] * (1.f - p));
+        for (int j = 0; j < 8; j++) {
+            float p, q;
+            logistic(g[j], &p, &q);
+            const float v = g[j] * p;
+            g[j] = d[j] * u[j] * p * (1.f + g[j] * q);
             u[j] *= v;
             d[j] *= v;
         }
-        store16v<DT>(dgate, r, c, n, false, g);
-        store16v<DT>(dup, r, c, n, false, d);
-        if (h.p) store16v<DT>(h, r, c, n, false, u);
+        if (n > 0) store_values<DT, PAST>(dgate.p, r * dgate.ld + c, n, false, g);
+        if (n > 0) store_values<DT, PAST>(dup.p, r * dup.ld + c, n, false, d);
+        if (h.p && n > 0) store_values<DT, PAST>(h.p, r * h.ld + c, n, false, u);
     });
 }
 
-template <int DT>
+template <int DT, int PAST>
 __global__ void __launch_bounds__(256)
 k_dequantize(Rows8 q, Mat y, bool f32, int R, int C, int cshift) {
-    for_blocks<4>(R, C, cshift, [&](int r, int c, auto n) {
-        float v[16];
-        values16(get_codes16(q.q + r * q.ld + c, n), q.scale[r * q.ld_scale + (c >> q.shift)], v);
-        store16v<DT>(y, r, c, n, f32, v);
+    for_blocks<3>(R, C, cshift, [&](int r, int c, auto n) {
+        float v[8];
+        values8(get_codes<PAST>(q.q + r * q.ld + c, n), q.scale[r * q.ld_scale + (c >> q.shift)], v);
+        if (n > 0) store_values<DT, PAST>(y.p, r * y.ld + c, n, f32, v);
     });
 }
 
 // ---- a scale for the row --------------------------------------------------
 // NT threads a row, 8 columns each and P times, kept in registers between the
 // maximum and the codes (P = 0: any number, made twice).
-template <int DT, bool F32>
+template <int DT, bool F32, int PAST>
 struct RowOf {
     Mat x;
-    BM_DEV void get(int64_t r, int c, int n, float (&v)[8]) const { load8<DT>(x.p, r * x.ld + c, n, F32, v); }
+    BM_DEV void get(int64_t r, int c, int n, float (&v)[8]) const { load_values<DT, PAST>(x.p, r * x.ld + c, n, F32, v); }
 };
-template <int DT>
+template <int DT, int PAST>
 struct SwigluOf {
     Mat gate, up;
     BM_DEV void get(int64_t r, int c, int n, float (&v)[8]) const {
         float u[8];
-        load8<DT>(gate.p, r * gate.ld + c, n, false, v);
-        load8<DT>(up.p, r * up.ld + c, n, false, u);
+        load_values<DT, PAST>(gate.p, r * gate.ld + c, n, false, v);
+        load_values<DT, PAST>(up.p, r * up.ld + c, n, false, u);
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = silu(v[j]) * u[j];
+        for (int j = 0; j < 8; j++) v[j] = silu_of(v[j]) * u[j];
     }
 };
 
@@ -349,34 +357,48 @@ int launch_quantize_rows(const bitmoe_rows &x, const bitmoe_rows8 &q, hipStream_
         constexpr int DT = dt.value;
         auto go = [&](auto f32) {
             constexpr bool F = decltype(f32)::value;
-            if (q.block == 0) return rows8_of(RowOf<DT, F>{mat(&x)}, out, x.rows, x.cols, s);
+            const int64_t bytes = (int64_t)x.rows * x.cols * (F ? 5 : 3);
+            if (q.block == 0) {
+                if (past_cache(bytes) == kCached) return rows8_of(RowOf<DT, F, kCached>{mat(&x)}, out, x.rows, x.cols, s);
+                return rows8_of(RowOf<DT, F, kLoadsPast>{mat(&x)}, out, x.rows, x.cols, s);
+            }
+            const Grid2 g = pieces_grid(x.rows, x.cols, 8, 4);
             return with_shift(q.block, [&](auto sh) {
-                const Grid2 g = pieces_grid(x.rows, x.cols, 16, 3);
-                k_quantize_blocks<DT, F, sh.value><<<g.grid, 256, 0, s>>>(mat(&x), out, x.rows, x.cols, g.cshift);
-                BM_LAUNCH_CHECK();
-                return BITMOE_OK;
+                return with_past(bytes, [&](auto past) {
+                    k_quantize_blocks<DT, F, sh.value, past.value><<<g.grid, 256, 0, s>>>(mat(&x), out, x.rows, x.cols, g.cshift);
+                    BM_LAUNCH_CHECK();
+                    return BITMOE_OK;
+                });
             });
         };
-        if (DT == BITMOE_F16 && x.dtype == BITMOE_F32) return go(std::true_type{});
+        if constexpr (DT == BITMOE_F16) {                      // (float32 is neither 16-bit type's)
+            if (x.dtype == BITMOE_F32) return go(std::true_type{});
+        }
         return go(std::false_type{});
     });
 }
 
 int launch_dequantize_rows(const bitmoe_rows8 &q, const bitmoe_rows &y, hipStream_t s) {
     return with_type(y.dtype, [&](auto dt) {
-        const Grid2 g = pieces_grid(q.q.rows, q.q.cols, 16, 3);
-        k_dequantize<dt.value><<<g.grid, 256, 0, s>>>(rows8(q), mat(&y), y.dtype == BITMOE_F32, q.q.rows, q.q.cols, g.cshift);
-        BM_LAUNCH_CHECK();
-        return BITMOE_OK;
+        const Grid2 g = pieces_grid(q.q.rows, q.q.cols, 8, 4);
+        return with_past((int64_t)y.cols * q.q.rows * (y.dtype == BITMOE_F32 ? 5 : 3), [&](auto past) {
+            k_dequantize<dt.value, past.value><<<g.grid, 256, 0, s>>>(rows8(q), mat(&y), y.dtype == BITMOE_F32, q.q.rows, q.q.cols, g.cshift);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        });
     });
 }
 
 int launch_swiglu_rows8(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows8 &q, hipStream_t s) {
     return with_type(gate.dtype, [&](auto dt) {
-        if (q.block == 0) return rows8_of(SwigluOf<dt.value>{mat(&gate), mat(&up)}, rows8(q), gate.rows, gate.cols, s);
-        const Grid2 g = pieces_grid(gate.rows, gate.cols, 16, 3);
+        if (q.block == 0) {
+            if (past_cache((int64_t)gate.rows * gate.cols * 5) == kCached)
+                return rows8_of(SwigluOf<dt.value, kCached>{mat(&gate), mat(&up)}, rows8(q), gate.rows, gate.cols, s);
+            return rows8_of(SwigluOf<dt.value, kLoadsPast>{mat(&gate), mat(&up)}, rows8(q), gate.rows, gate.cols, s);
+        }
+        const Grid2 g = pieces_grid(gate.rows, gate.cols, 8, 4);
         return with_shift(q.block, [&](auto sh) {
-            k_swiglu_blocks<dt.value, sh.value><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), rows8(q), gate.rows, gate.cols, g.cshift);
+            k_swiglu_blocks<dt.value, sh.value, kCached><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), rows8(q), gate.rows, gate.cols, g.cshift);
             BM_LAUNCH_CHECK();
             return BITMOE_OK;
         });
@@ -385,13 +407,15 @@ int launch_swiglu_rows8(const bitmoe_rows &gate, const bitmoe_rows &up, const bi
 
 int launch_swiglu_checkpoint(const bitmoe_rows &gate, const bitmoe_rows &up, const bitmoe_rows &h,
                              const bitmoe_rows8 &gate8, const bitmoe_rows8 &up8, hipStream_t s) {
-    const Grid2 g = pieces_grid(gate.rows, gate.cols, 16, 3);
+    const Grid2 g = pieces_grid(gate.rows, gate.cols, 8, 4);
     return with_type(gate.dtype, [&](auto dt) {
         return with_shift(gate8.block, [&](auto sh) {
-            k_swiglu_checkpoint<dt.value, sh.value><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), mat(&h), rows8(gate8),
-                                                                         rows8(up8), gate.rows, gate.cols, g.cshift);
-            BM_LAUNCH_CHECK();
-            return BITMOE_OK;
+            return with_past((int64_t)gate.rows * gate.cols * 8, [&](auto past) {
+                k_swiglu_checkpoint<dt.value, sh.value, past.value><<<g.grid, 256, 0, s>>>(
+                    mat(&gate), mat(&up), mat(&h), rows8(gate8), rows8(up8), gate.rows, gate.cols, g.cshift);
+                BM_LAUNCH_CHECK();
+                return BITMOE_OK;
+            });
         });
     });
 }
@@ -399,12 +423,14 @@ int launch_swiglu_checkpoint(const bitmoe_rows &gate, const bitmoe_rows &up, con
 int launch_swiglu_checkpoint_backward(const bitmoe_rows &dh, const bitmoe_rows8 &gate8, const bitmoe_rows8 &up8,
                                       const bitmoe_rows &dgate, const bitmoe_rows &dup, const bitmoe_rows *h,
                                       hipStream_t s) {
-    const Grid2 g = pieces_grid(dh.rows, dh.cols, 16, 3);
+    const Grid2 g = pieces_grid(dh.rows, dh.cols, 8, 4);
     return with_type(dh.dtype, [&](auto dt) {
-        k_swiglu_checkpoint_backward<dt.value><<<g.grid, 256, 0, s>>>(mat(&dh), rows8(gate8), rows8(up8), mat(&dgate),
-                                                                     mat(&dup), mat(h), dh.rows, dh.cols, g.cshift);
-        BM_LAUNCH_CHECK();
-        return BITMOE_OK;
+        return with_past((int64_t)dh.rows * dh.cols * (h ? 10 : 8), [&](auto past) {
+            k_swiglu_checkpoint_backward<dt.value, past.value><<<g.grid, 256, 0, s>>>(
+                mat(&dh), rows8(gate8), rows8(up8), mat(&dgate), mat(&dup), mat(h), dh.rows, dh.cols, g.cshift);
+            BM_LAUNCH_CHECK();
+            return BITMOE_OK;
+        });
     });
 }
 

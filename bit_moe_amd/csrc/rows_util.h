@@ -89,4 +89,53 @@ BM_DEV void put(const Mat &m, int64_t r, int c, int cols, bool f32, const float 
     store8<DT>(m.p, r * m.ld + c, FULL ? 8 : cols - c, f32, v);
 }
 
+// eight values of a row of DT or float32, the first n of them (the rest 0; none
+// read for n <= 0), and back
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+template <int DT, int PAST>
+BM_DEV void load_values(const void *p, int64_t i, int n, bool f32, float *v) {
+    if (n >= 8 && PAST != kCached) {
+        if (f32) {
+            const f32x4_any *q = reinterpret_cast<const f32x4_any *>(static_cast<const float *>(p) + i);
+            const f32x4_any a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                v[j] = a[j];
+                v[4 + j] = b[j];
+            }
+        } else {
+            const u32x4_any u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(static_cast<const uint16_t *>(p) + i));
+            values<DT>(make_uint4(u[0], u[1], u[2], u[3]), v);
+        }
+    } else {
+        load8<DT>(p, i, n, f32, v);
+    }
+}
+template <int DT, int PAST>
+BM_DEV void store_values(void *p, int64_t i, int n, bool f32, const float *v) {
+    if (n >= 8 && PAST == kAllPast) {
+        if (f32) {
+            f32x4_any *q = reinterpret_cast<f32x4_any *>(static_cast<float *>(p) + i);
+            __builtin_nontemporal_store(f32x4_any{v[0], v[1], v[2], v[3]}, q);
+            __builtin_nontemporal_store(f32x4_any{v[4], v[5], v[6], v[7]}, q + 1);
+        } else {
+            u32x4_any u;
+#pragma unroll
+            for (int j = 0; j < 4; j++) u[j] = elem_pair<DT>(v[2 * j], v[2 * j + 1]);
+            __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(p) + i));
+        }
+    } else {
+        store8<DT>(p, i, n, f32, v);
+    }
+}
+// f(past) for the bytes that a call moves
+template <class F>
+int with_past(int64_t bytes, F f) {
+    switch (past_cache(bytes)) {
+        case kCached: return f(std::integral_constant<int, kCached>{});
+        case kLoadsPast: return f(std::integral_constant<int, kLoadsPast>{});
+        default: return f(std::integral_constant<int, kAllPast>{});
+    }
+}
+
 }  // namespace bm
