@@ -11,7 +11,10 @@ using bm_host::GemmPlan;
 
 // Rows of K codes at any address to rows of ld, whole 16-byte pieces with zeros
 // behind K, at `to`: the call's rows of x (with their scales) that lie in a group,
-// and the rows of W of the experts that have some.  A wave a row.
+// and the rows of W of the experts that have some.  A wave a row, a word a lane: the
+// word of memory that holds its first code and, where it is not all of them, the
+// next one (neighbouring lanes' words are one access; 16 bytes a lane at an odd
+// address take several times an even one's).  No word without a code is read.
 __global__ void __launch_bounds__(256)
 k_i8_pack(GemmArgs g, uint8_t *x, float *scale, uint8_t *w, int ld) {
     const int lane = threadIdx.x & 63, r0 = group_start(g, 0), r1 = group_start(g, g.E);
@@ -32,7 +35,24 @@ k_i8_pack(GemmArgs g, uint8_t *x, float *scale, uint8_t *w, int ld) {
             from = static_cast<const uint8_t *>(g.b.p) + (int64_t)e * g.b_stride + (int64_t)n * g.b.ld;
             to = w + (i - g.R) * ld;
         }
-        for (int k = lane * 16; k < ld; k += 64 * 16) *reinterpret_cast<uint4 *>(to + k) = load_codes(from, k, g.K);
+        const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3), K = from ? g.K : 0;
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(from - off);
+        for (int j0 = 0; j0 < ld / 4; j0 += 256) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int j = j0 + 64 * u + lane;
+                lo[u] = 4 * j < K ? words[j] : 0;
+                hi[u] = off && 4 * j + 4 - off < K ? words[j + 1] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int j = j0 + 64 * u + lane, left = K - 4 * j;
+                uint32_t v = __builtin_amdgcn_alignbyte(hi[u], lo[u], off);
+                if (left < 4) v = left > 0 ? v & ((1u << (8 * left)) - 1) : 0;
+                if (j < ld / 4) *reinterpret_cast<uint32_t *>(to + 4 * j) = v;
+            }
+        }
     }
 }
 

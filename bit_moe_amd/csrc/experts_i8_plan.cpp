@@ -46,8 +46,8 @@ const Shape kShapes[] = {
     {kTile128, 128, 128, 2, 0.77, 9.4, 0.40},
     {kTile64x128, 64, 128, 2, 0.525, 5.6, 0.45},
 };
-// (its loads wait for one another: a workgroup alone is no faster)
-const Shape kAnyShape = {kAny, 128, 128, 2, 1.40, 5.0, 1.0};
+// (its loads wait for one another: a workgroup alone is slower)
+const Shape kAnyShape = {kAny, 128, 128, 2, 1.40, 5.0, 1.4};
 
 }  // namespace
 
@@ -112,7 +112,7 @@ GemmPlan i8_plan(const GemmArgs &g, bool whole) {
         // product takes laid on 16 bytes first, up to 1 GiB of them
         const size_t packed = i8_pack(g.E, g.R, g.N, g.K).bytes;
         if (g.K % 16 && packed <= (size_t)1 << 30) {
-            const double before = 4 + ((double)g.R * g.K + weights) * 2 / 3e6;
+            const double before = 3 + ((double)g.R * g.K + weights) * 2 / 5e6;
             for (const Shape &s : kShapes) tiles_of(s, before, true);
         }
     }
