@@ -5,7 +5,9 @@
 
 namespace bm {
 
-// the scale of the call's row r (0 for one that the map does not give)
+// the scale of expert e's output n (of the last one, past it), and of the call's row
+// r (0 for one that the map does not give)
+BM_DEV float col_scale(const GemmArgs &g, int e, int n) { return g.b_scale[e * g.b_scale_stride + min(n, g.N - 1)]; }
 BM_DEV float row_scale(const GemmArgs &g, int r) {
     const int row = row_of(g.a, r);
     return row >= 0 ? g.a_scale[row * g.a_ld_scale] : 0.f;
@@ -14,10 +16,12 @@ BM_DEV float row_scale(const GemmArgs &g, int r) {
 // The waves' int32 sums to memory, as tile_epilogue does it: a lane's 4 columns
 // of a row become 8 through LDS.  A value is (sum * row's scale) * column's
 // scale in fp32, rounded once to its type; the sum to fp32 is one rounding more
-// (from 2^24).  srow, sscale: output row (or -1) and scale of each of the tile's rows.
+// (from 2^24).  srow, sscale, scol: output row (or -1) and scale of each of the tile's
+// rows, scale of each of its columns (in LDS: a load here would wait for those of the
+// next tile, which are on their way).
 template <int DT, int BM, int BN, int HALVES, int TM, int TN>
 BM_DEV void i8_epilogue(const GemmArgs &g, const i32x4 (&acc)[TM][TN], float *lds, const int *srow, const float *sscale,
-                        int e, int split, int n0, int m_at, int n_at, int wave, int lane) {
+                        const float *scol, int split, int n0, int m_at, int n_at, int wave, int lane) {
     constexpr int MR = 16 * TM / HALVES, TH = TN / 2, CW = 16 * TH;      // columns at a time
     constexpr int LDW = CW + 4, LPR = CW / 8, RPI = 64 / LPR, IT = 16 / RPI;
     int *sw = reinterpret_cast<int *>(lds) + wave * epilogue_floats<TN>();
@@ -28,7 +32,7 @@ BM_DEV void i8_epilogue(const GemmArgs &g, const i32x4 (&acc)[TM][TN], float *ld
     for (int h = 0; h < 2; h++)
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            cs[h][j] = g.raw ? 1.f : g.b_scale[e * g.b_scale_stride + min(nn[h] + j, g.N - 1)];
+            cs[h][j] = scol[nn[h] - n0 + j];
 #pragma unroll
     for (int q = 0; q < TM; q++) {
         int rows[IT];
@@ -91,7 +95,7 @@ k_i8_any(GemmArgs g, int mtiles, int ntiles) {
     __shared__ __attribute__((aligned(16))) uint16_t lds[(BM + BN) * kBK];
     static_assert(sizeof(lds) >= 4 * epilogue_floats<TN>() * 4, "");
     __shared__ int srow[BM];
-    __shared__ float sscale[BM];
+    __shared__ float sscale[BM], scol[BN];
     uint16_t *sa = lds, *sb = lds + BM * kBK;
     Tile t;
     Tiles<kForward, BM> list;
@@ -122,6 +126,7 @@ k_i8_any(GemmArgs g, int mtiles, int ntiles) {
     };
     set_rows<kForward, BM>(g, t, m0, tid, srow);
     if (tid < BM) sscale[tid] = !g.raw && m0 + tid < t.r1 - t.r0 ? row_scale(g, t.r0 + m0 + tid) : 0.f;
+    if (tid < BN) scol[tid] = g.raw ? 0.f : col_scale(g, t.e, n0 + tid);
     i32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; i++)
@@ -150,7 +155,7 @@ k_i8_any(GemmArgs g, int mtiles, int ntiles) {
         __syncthreads();
     }
     __syncthreads();         // (srow, where the loop did not run)
-    i8_epilogue<DT, BM, BN, 1>(g, acc, reinterpret_cast<float *>(lds), srow, sscale, t.e, k.split, n0, wm * 64, wn * 64,
+    i8_epilogue<DT, BM, BN, 1>(g, acc, reinterpret_cast<float *>(lds), srow, sscale, scol, k.split, n0, wm * 64, wn * 64,
                                wave, lane);
 }
 

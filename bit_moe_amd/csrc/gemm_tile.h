@@ -83,14 +83,15 @@ BM_DEV void phase_barrier() {
 
 // Dynamic LDS of a workgroup: two stages; the output rows of this tile and the
 // next; A's rows; for the weights' gradient a ring of row maps (64 of A's, 64 of
-// B's, four stages); in 8 bits the rows' scales; the epilogue's part, which is its own, so that the next
+// B's, four stages); in 8 bits the rows' and the
+// columns' scales; the epilogue's part, which is its own, so that the next
 // tile's first stages can be on their way during it.
 template <int LAY, int DT, int BM, int BN, int WM, int WN, bool MAPS>
 struct TileLds {
     static constexpr int rows = 2 * (BM + BN) * kBK * 2;
     static constexpr int maps = rows + 3 * BM * 4;
     static constexpr int scales = maps + (MAPS ? 4 * 128 * 4 : 0);
-    static constexpr int out = scales + (DT >= kI8 ? 2 * BM * 4 : 0);
+    static constexpr int out = scales + (DT >= kI8 ? 2 * (BM + BN) * 4 : 0);
     static constexpr int bytes = out + WM * WN * epilogue_floats<BN / WN / 16>() * 4;
     static_assert(bytes <= 160 * 1024, "");
 };
@@ -140,7 +141,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
     static_assert(LAY == kForward || DT < kI8, "");
     static_assert((LAY == kGradWeights || !MAPS) && (LAY == kForward || MAPS ? !PARTS : true), "");
     constexpr int kUA = UM * kBK, kUB = UN * kBK, kStage = 2 * (kUA + kUB);       // elements
-    static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW, "");
+    static_assert(PA >= 1 && PB >= 1 && TI >= 1 && TJ >= 1 && BM <= 64 * NW && (DT < kI8 || BN <= 64 * NW), "");
     extern __shared__ __attribute__((aligned(1024))) uint16_t lds[];
     Tile t;
     Tiles<LAY, BM> list;
@@ -231,6 +232,7 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         set_rows<LAY, BM>(g, t, m0, tid, srow + par * BM);
         if (DT >= kI8 && tid < BM)
             sscale[par * BM + tid] = !g.raw && m0 + tid < t.r1 - t.r0 ? row_scale(g, t.r0 + m0 + tid) : 0.f;
+        if (DT >= kI8 && tid < BN) sscale[2 * BM + par * BN + tid] = g.raw ? 0.f : col_scale(g, t.e, n0 + tid);
     };
     // MAPS: the rows that the maps give (g.arows, g.brows), fetched two stages
     // before the loads that go by them; a stage's offsets are made at the
@@ -438,8 +440,8 @@ k_gemm_tile(GemmArgs g, int mtiles, int ntiles) {
         if (again) continue;
         float *through = reinterpret_cast<float *>(reinterpret_cast<char *>(lds) + TileLds<LAY, DT, BM, BN, WM, WN, MAPS>::out);
         if constexpr (DT >= kI8)
-            i8_epilogue<DT, BM, BN, 2>(g, acc, through, srow + par * BM, sscale + par * BM, e, part, n, wm * (UM / WM),
-                                       wn * (UN / WN), wave, lane);
+            i8_epilogue<DT, BM, BN, 2>(g, acc, through, srow + par * BM, sscale + par * BM, sscale + 2 * BM + par * BN, part,
+                                       n, wm * (UM / WM), wn * (UN / WN), wave, lane);
         else
             tile_epilogue<LAY, DT, BM, BN, 2>(g, acc, through, srow + par * BM, e, part, n, wm * (UM / WM),
                                               wn * (UN / WN), wave, lane);

@@ -9,6 +9,7 @@
 // <g w_a o, ds>, <g w_a o, p> and <g w_a o, s>, which do not need t.
 #pragma once
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "norm.h"
@@ -77,9 +78,9 @@ BM_DEV void store_cols(const NormMat &m, int64_t r, int c, int n, const float (&
 
 template <int DT, int P>
 __global__ void __launch_bounds__(1024)
-k_block_norm(NormArgs a) {
+k_block_norm(NormArgs a, int r0) {
     __shared__ float part[4][kMost][8];
-    const int64_t r = blockIdx.x;
+    const int64_t r = r0 + (int64_t)blockIdx.x;
     float v[P][8], o[P][8];
     auto col = [&](int p) { return (int)(threadIdx.x + p * blockDim.x) * 8; };
     auto left = [&](int p) { return a.H - col(p); };
@@ -411,9 +412,13 @@ inline int64_t norm_bytes(int T, int H, std::initializer_list<const NormMat *> m
 template <int DT>
 int launch_norm(const NormArgs &a, hipStream_t st) {
     const int pieces = a.H <= 8192 ? 1 : 2, threads = (a.H + pieces * 512 - 1) / (pieces * 512) * 64;
-    if (pieces == 1) k_block_norm<DT, 1><<<a.T, threads, 0, st>>>(a);
-    else k_block_norm<DT, 2><<<a.T, threads, 0, st>>>(a);
-    BM_LAUNCH_CHECK();
+    constexpr int most = 1 << 21;               // (a launch holds less than 2^32 threads)
+    for (int r0 = 0; r0 < a.T; r0 += most) {
+        const int rows = std::min(a.T - r0, most);
+        if (pieces == 1) k_block_norm<DT, 1><<<rows, threads, 0, st>>>(a, r0);
+        else k_block_norm<DT, 2><<<rows, threads, 0, st>>>(a, r0);
+        BM_LAUNCH_CHECK();
+    }
     return BITMOE_OK;
 }
 
