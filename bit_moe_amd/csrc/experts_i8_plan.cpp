@@ -109,9 +109,9 @@ GemmPlan i8_plan(const GemmArgs &g, bool whole) {
     } else {
         tiles_of(kAnyShape, 0, false);
         // Odd K, where the addresses cannot help it: the operands' rows that the
-        // product takes laid on 16 bytes first, up to 1 GiB of them
+        // product takes laid on 16 bytes first, up to 4 GiB of them
         const size_t packed = i8_pack(g.E, g.R, g.N, g.K).bytes;
-        if (g.K % 16 && packed <= (size_t)1 << 30) {
+        if (g.K % 16 && packed <= (size_t)4 << 30) {
             const double before = 3 + ((double)g.R * g.K + weights) * 2 / 5e6;
             for (const Shape &s : kShapes) tiles_of(s, before, true);
         }
