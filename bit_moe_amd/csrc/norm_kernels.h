@@ -153,8 +153,8 @@ BM_DEV void fetch(const NormMat &m, int64_t r, int c, int n, Piece<WIDE> &q) {
         q.lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
         q.hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     } else {
-        const Mat t{m.p, m.ld};
-        q.lo = n >= 8 ? piece<true, PAST>(t, r, c, 0) : piece<false, PAST>(t, r, c, c + n);
+        q.lo = n >= 8 ? piece<true, PAST>(Mat{m.p, m.ld}, r, c, 0)
+                      : load_part(static_cast<const uint16_t *>(m.p) + r * m.ld + c, n);
     }
 }
 template <int DT, bool WIDE>

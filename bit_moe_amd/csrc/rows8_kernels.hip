@@ -77,9 +77,14 @@ BM_DEV uint2 get_codes(const int8_t *p, int n) {
         return make_uint2(u[0], u[1]);
     }
     uint32_t w[2] = {0, 0};
+    if (n > 0) {
+        // (all loads at once: load_part)
+        uint32_t e[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-        if (j < n) w[j >> 2] |= (uint32_t)(uint8_t)p[j] << (8 * (j & 3));
+        for (int j = 0; j < 8; j++) e[j] = (uint8_t)p[min(j, n - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j >> 2] |= j < n ? e[j] << (8 * (j & 3)) : 0;
+    }
     return make_uint2(w[0], w[1]);
 }
 BM_DEV void values8(const uint2 &u, float scale, float (&v)[8]) {
