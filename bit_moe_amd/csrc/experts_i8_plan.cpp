@@ -21,9 +21,8 @@
 //  the same, 8 each, N 4096                 1229     1254    1227             1
 //  8 groups of 1 row, N 4096, K 7168                          44.7     51.9
 //  one row, N 16384, K 4096                                   21.6     17.7
-//  codes not on 16 bytes: 8192 x 4096 x 7168 283 (aligned, forced), 8192 x 2049 x
-//   7167 255, 333 x 1001 x 2047 in parts 1, 2, 4, 8: 37.3 33.6 30.4 28.9, 16 x 2049 x
-//   7167 70.0 47.5 33.5 26.4 26.4
+//  codes not on 16 bytes, as they lie and laid out anew: 8192 x 2049 x 7167 270, 161; 8
+//   groups, 666 rows, 1001 x 2047 33.7 (4 parts), 24.3; 16 x 2049 x 7167 26.4 (16 parts)
 #include <algorithm>
 #include <cmath>
 

@@ -42,7 +42,10 @@ int launch_block_norm_backward_f16(const NormBackArgs &a, hipStream_t st);
 // of a workgroup, and workgroups, each of which leaves a slice of partial sums.  8
 // columns a thread up to 2048, 16 above, in workgroups of 4 waves, or as many as a row
 // needs; so many of them as run at a time (3, 2, 1 on a compute unit, by their
-// registers).
+// registers).  us, 8 and 16 columns a thread: 16384 x 512 51.3 and 53.5, x 2048 96.7 and
+// 101.2, x 4096 177 (a workgroup of 512 threads a compute unit) and 174 (two of 256),
+// 8192 x 7168 183 (14 waves of few registers, which spill) and 169.  Above 8192 columns the
+// registers spill (2048 x 16384 560).
 struct NormShape {
     int pieces, nt, groups, slices;
 };

@@ -7,6 +7,11 @@
 // 8 columns a piece, and stays in their registers from the sums to the outputs.  The
 // backward pass needs all its sums in one step: <v, o> is taken apart into
 // <g w_a o, ds>, <g w_a o, p> and <g w_a o, s>, which do not need t.
+// Bound by memory: 8192 x 7168 with a gate by channel and a float32 stream forward 137 us
+// (5.1 TB/s), in 16 bits backward 153 (4.6), with a gate by token 193 (4.9); 3001 x 2047
+// forward 22 us, backward 49.  The forward pass goes through the memory-side cache (134
+// to 140 us against 147 past it), the backward pass reads past it where a call moves more
+// than it holds (158 us against 171).
 #pragma once
 
 #include <algorithm>

@@ -10,7 +10,11 @@
 // quotient that float32 holds comes out as it is.  m and x are first taken to m's own
 // power of two, so nothing overflows on the way.
 // Bound by memory, and close behind it by the arithmetic of a code (9 operations) and
-// of silu.
+// of silu: 65536 x 2048 with its inputs kept forward 162 to 180 us, backward 168 (6.5 TB/s
+// together), 16384 x 7168 to codes 64 us and back 54, 8192 x 7168 by rows 29.  8 columns
+// a thread: 16 make a store past the cache half a line (the backward pass 299 us against
+// 219 before its other steps).  The codes are stored through the cache, where what reads
+// them next finds them.
 #include "rows8.h"
 #include "rows_util.h"
 
@@ -327,16 +331,19 @@ int rows8_by(const S &src, const Rows8 &q, int R, int C, hipStream_t s) {
     }
     return BITMOE_OK;
 }
-// A wave a row where there are rows enough and its registers hold one.
+// Threads of a row and pieces of 8 columns of each, which registers hold (none: the
+// row is read twice).  us, the one taken first: rows of 1024 columns, 16384 of them,
+// 64 x 2 12.3, 256 x 1 16.6, 64 x 4 12.9; of 2048, 32768 rows, 256 x 1 41.9, 64 x 4 40.5,
+// 64 x 8 42.7, 1024 x 1 96, from gate and up 55.5, 58.5, 71.2, 138; of 4096, 16384 rows,
+// 256 x 4 37.5, 64 x 8 45.1, 1024 x 1 56.9; of 7168, 16384 rows, 256 x 4 60, 1024 x 1 72.5,
+// 1024 x 4 92.6, 256 rows 1024 x 1 3.5, 256 x 4 4.4; of 16384, 2048 rows, 1024 x 4 23.1,
+// read twice 25.2.
 template <class S>
 int rows8_of(const S &src, const Rows8 &q, int R, int C, hipStream_t s) {
     if (C > 32768) return rows8_by<1024, 0>(src, q, R, C, s);
     if (C > 8192) return rows8_by<1024, 4>(src, q, R, C, s);
-    if (R < 1024 && C > 2048) return rows8_by<1024, 1>(src, q, R, C, s);
-    if (R < 1024 && C > 512) return rows8_by<256, 1>(src, q, R, C, s);
-    if (C > 4096) return rows8_by<256, 4>(src, q, R, C, s);
-    if (C > 2048) return rows8_by<64, 8>(src, q, R, C, s);
-    if (C > 1024) return rows8_by<64, 4>(src, q, R, C, s);
+    if (C > 2048) return R < 1024 ? rows8_by<1024, 1>(src, q, R, C, s) : rows8_by<256, 4>(src, q, R, C, s);
+    if (C > 1024) return rows8_by<256, 1>(src, q, R, C, s);
     return rows8_by<64, 2>(src, q, R, C, s);
 }
 
