@@ -1,5 +1,6 @@
 """bit_moe_amd: the 2-bit (and MXFP4) routed-expert MoE FFN layer on MI355X (gfx950),
-and the operators of the same layer with 16-bit experts and their gradients.
+the operators of the same layer with 16-bit experts and their gradients, its products
+and activations in 8 bits, and the norms around a block.
 
 Python binding over libbitmoe.so (see include/bitmoe.h).  PyTorch provides
 device memory and streams only; every step of the layer runs in the
