@@ -192,3 +192,29 @@ def test_norm_backward_rows_in_turn(bm, T, H, groups, most, dtype, stream, gate)
     huge = [0, step, groups + step + 1, 2 * groups, 2 * groups + 2 * step, 3 * groups + groups - 1, T - 1] if dtype is BF else []
     assert all(r < T for r in huge) and 2 * step < T <= 3 * step
     norm_backward(bm, T, H, 0, dtype, stream, gate, huge)
+
+
+def test_gates_far_below_zero(bm):
+    """silu(z) down to float32's smallest normal value (z = -92), and past it: e^z is
+    itself below that from z = -87.3.  Behind its relative error a value has float32's and
+    bfloat16's steps near 0 (2^-149 times what it is taken times; half of 2^-133)."""
+    z = -torch.arange(80, 106, 0.5)
+    gate = z[:, None].repeat(1, 96).to(BF).cuda()
+    up, dh = rnd(gen(7), z.numel(), 96, BF), rnd(gen(8), z.numel(), 96, BF)
+    g, u, d = gate.double(), up.double(), dh.double()
+    half, zero = ex.half_ulp(BF) * (1 + 2.0 ** -8), 2.0 ** -134
+    say("[ranges] gates from -80 to -105.5")
+    h, g8, u8 = bm.swiglu_checkpoint(gate, up, block=32)
+    want = ex.swiglu(g, u)
+    near(h, want, (half + r8.silu_bound(g) + r8.U) * want.abs() + (u.abs() * (1 - g) + 1) * 2.0 ** -149 + zero, "h")
+    q = bm.swiglu_rows8(gate, up, block=32)
+    e = (r8.silu_bound(g) + r8.U) * want.abs() + (u.abs() * (1 - g) + 1) * 2.0 ** -149
+    scale = r8.quantize(want, 32)[2]
+    near(q.scale, scale, r8.blocks_of(e, 32).amax(2) / 127 + r8.U * scale + 2.0 ** -149, "scales")
+    dg, du, h8 = bm.swiglu_checkpoint_backward(dh, g8, u8, need_h=True)
+    gk, uk = (r8.values(x.codes.double(), x.scale.double(), 32) for x in (g8, u8))
+    wg, wu = ex.swiglu_backward(d, gk, uk)
+    wh = ex.swiglu(gk, uk)
+    near(dg, wg, half * wg.abs() + r8.slope_bound(d, gk, uk) + ((d * uk).abs() + 1) * (1 - gk) * 2.0 ** -148 + zero, "dgate")
+    near(du, wu, (half + r8.silu_bound(gk) + 3 * r8.U) * wu.abs() + (d.abs() * (1 - gk) + 1) * 2.0 ** -149 + zero, "dup")
+    near(h8, wh, (half + r8.silu_bound(gk) + 3 * r8.U) * wh.abs() + (uk.abs() * (1 - gk) + 1) * 2.0 ** -149 + zero, "h again")
