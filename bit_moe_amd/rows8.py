@@ -197,7 +197,8 @@ def expert_matmul_i8(x, w, offsets=None, x_rows=None, x_div=1, y_rows=None, y=No
 
 def swiglu_rows8(gate, up, block=0, out=None, stream=None):
     """h = silu(gate) * up straight into 8 bits (Rows8 [R, I], as
-    quantize_rows'), for a down projection by expert_matmul_i8."""
+    quantize_rows'): with block 0 for a down projection by expert_matmul_i8, with
+    another block to be kept and read back by dequantize_rows."""
     given = () if out is None else (out.codes, out.scale)
     dev = _device(gate, up, *given)
     there = _elsewhere(dev, stream)
@@ -346,7 +347,8 @@ def block_norm_backward(dn=None, ds=None, s=None, o=None, w_after=None, gate=Non
     """Gradients of block_norm, a BlockNormGrads: dn [T, H] is n's gradient, ds
     [T, H] that of s from the stream's later uses (one may be None), s and o what
     the forward call gave and had (s with dn; o None if it had none), the rest as
-    there.  dresidual is of ds's type (without it dn's) if not given; dw_after,
+    there.  dresidual is of ds's type (without it dn's: for the last norm of a
+    stream in float32, give one in float32) if not given; dw_after,
     dw_before [H] and the gradient of a gate [H] are sums over tokens in out_dtype
     (default the 16-bit type, or that of a given one; float32 allowed), that of a
     gate [T, H] is of its type.  need_dw: the weights' and the gate's, where the

@@ -594,12 +594,16 @@ int moe_combine_backward(const bitmoe_rows *dy, const bitmoe_rows *o, const floa
  * block of a row may be shorter) or, with block 0, one for the whole row.  For
  * the values x of a block and m their largest magnitude
  *     scale = m / 127,  code = rint(127 x / m)   (ties to even),
- * so a code stands for code * scale, within scale / 2 of x (m >= 2^-110,
- * below which the scale's own rounding shows), and is -127 .. 127.
+ * so a code is -127 .. 127 and stands for code * scale, within scale (1/2 + 2^-15) of
+ * x (2^-15: the roundings of the scale, taken code times, and of the quotient; m >=
+ * 2^-110, below which the scale's rounding shows more).
  * A block of zeros has scale 0; scale is rounded down where code * scale would be
  * infinite (m the largest float32); one that holds an infinity or NaN has scale NaN
- * and codes 0 (it stands for NaN throughout).  127 x / m is rounded to float32
- * once before rint, which for 16-bit x never changes a code.
+ * and codes 0 (it stands for NaN throughout).  For 16-bit x the codes are those of
+ * exact arithmetic: 127 x / m is rounded to float32 once before rint, which changes
+ * none of them.  For float32 x (and SwiGLU's h) 127 x is rounded and then the
+ * quotient: where that is within 127 2^-23 of a tie, a code may be its other
+ * neighbour.
  *
  * Conventions are those of the 16-bit expert layer above (sizes, maps, streams,
  * workspaces, errors), and:
