@@ -1,6 +1,6 @@
 // Products in 8 bits: their epilogue, and the kernels for codes of any alignment and
-// for few rows.  8192^3 391 us in the tile kernel (2.8 POPS), 8192 x 4096 x 7168 188
-// (2.55), 256 groups of 64 rows at 5.5 TB/s.
+// for few rows.  8192^3 391 to 422 us in the tile kernel from run to run (2.8 to 2.6 POPS),
+// 8192 x 4096 x 7168 184 to 192 (2.6 to 2.5), 256 groups of 64 rows at 5.5 TB/s.
 #pragma once
 
 #include "gemm_util.h"

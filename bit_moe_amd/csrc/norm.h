@@ -41,11 +41,14 @@ int launch_block_norm_backward_f16(const NormBackArgs &a, hipStream_t st);
 // The backward pass's launch: pieces of 8 columns a thread, threads of a row, rows
 // of a workgroup, and workgroups, each of which leaves a slice of partial sums.  8
 // columns a thread up to 2048, 16 above, in workgroups of 4 waves, or as many as a row
-// needs; so many of them as run at a time (3, 2, 1 on a compute unit, by their
-// registers).  us, 8 and 16 columns a thread: 16384 x 512 51.3 and 53.5, x 2048 96.7 and
+// needs; so many of them as run at a time (3, 2, 1 on a compute unit, by most instances'
+// registers).  With a float32 stream and a gate by token 2 run where the rule takes 3:
+// 16384 x 2048 183 us in its 768 slices, 149 in 512, 3001 x 2047 76 and 61; the others 92 and
+// 89 (gate by channel), 119 and 110 (by token), 3001 x 2047 38 and 40, 50 and 55 (the rule
+// does not know the instance).  us, 8 and 16 columns a thread: 16384 x 512 51.3 and 53.5, x 2048 96.7 and
 // 101.2, x 4096 177 (a workgroup of 512 threads a compute unit) and 174 (two of 256),
 // 8192 x 7168 183 (14 waves of few registers, which spill) and 169.  Above 8192 columns the
-// registers spill (2048 x 16384 560).
+// registers spill (2048 x 16384 560 to 810).
 struct NormShape {
     int pieces, nt, groups, slices;
 };

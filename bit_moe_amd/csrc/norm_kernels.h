@@ -7,11 +7,15 @@
 // 8 columns a piece, and stays in their registers from the sums to the outputs.  The
 // backward pass needs all its sums in one step: <v, o> is taken apart into
 // <g w_a o, ds>, <g w_a o, p> and <g w_a o, s>, which do not need t.
-// Bound by memory: 8192 x 7168 with a gate by channel and a float32 stream forward 137 us
-// (5.1 TB/s), in 16 bits backward 153 (4.6), with a gate by token 193 (4.9); 3001 x 2047
-// forward 22 us, backward 49.  The forward pass goes through the memory-side cache (134
-// to 140 us against 147 past it), the backward pass reads past it where a call moves more
-// than it holds (158 us against 171).
+// Bound by memory: 8192 x 7168 with a gate by channel forward 106 us (4.5 TB/s), with a
+// float32 stream 140 (5.0), backward 145 (4.9) and 250 (4.2), with a gate by token 192 (4.9)
+// and 342 (3.8: 25 registers spill).  3001 x 2047, rows that are not on 16 bytes, forward 15
+// to 20 us (3.2 to 4.2 TB/s), backward 35 to 42 (2.1 to 2.6), with a float32 stream and a
+// gate by token 69.  (us a call, calls one after another on changing inputs.)  Above 8192
+// columns the backward pass spills 380 to 498 registers: 2048 x 16384 560 to 810 us (0.7 to
+// 1.0 TB/s).  The forward pass goes through the memory-side cache (134 to 140 us against
+// 147 past it), the backward pass reads past it where a call moves more than it holds (158
+// us against 171).
 #pragma once
 
 #include <algorithm>

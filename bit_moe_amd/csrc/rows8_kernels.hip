@@ -10,8 +10,10 @@
 // quotient that float32 holds comes out as it is.  m and x are first taken to m's own
 // power of two, so nothing overflows on the way.
 // Bound by memory, and close behind it by the arithmetic of a code (9 operations) and
-// of silu: 65536 x 2048 with its inputs kept forward 162 to 180 us, backward 168 (6.5 TB/s
-// together), 16384 x 7168 to codes 64 us and back 54, 8192 x 7168 by rows 29.  8 columns
+// of silu: 65536 x 2048 with its inputs kept forward 192 us, backward 182, one after the
+// other 345 (6.3 TB/s); 16384 x 7168 to codes 67 us and back 61, one after the other 117,
+// by rows 66, 8192 x 7168 by rows 33; silu into codes 65536 x 2048 by rows 115 us, in
+// blocks 114.  (us a call, calls one after another on changing inputs.)  8 columns
 // a thread: 16 make a store past the cache half a line (the backward pass 299 us against
 // 219 before its other steps).  The codes are stored through the cache, where what reads
 // them next finds them.
@@ -413,6 +415,8 @@ int launch_swiglu_rows8(const bitmoe_rows &gate, const bitmoe_rows &up, const bi
                 return rows8_of(SwigluOf<dt.value, kCached>{mat(&gate), mat(&up)}, rows8(q), gate.rows, gate.cols, s);
             return rows8_of(SwigluOf<dt.value, kLoadsPast>{mat(&gate), mat(&up)}, rows8(q), gate.rows, gate.cols, s);
         }
+        // (through the cache at any size.  Past it, us: 16384 x 2048 33.3 and 33.3, 32768 rows
+        // 56.1, 61.6 through it, 65536 rows 115 and 118, 16384 x 7168 108 and 108)
         const Grid2 g = pieces_grid(gate.rows, gate.cols, 8, 4);
         return with_shift(q.block, [&](auto sh) {
             k_swiglu_blocks<dt.value, sh.value, kCached><<<g.grid, 256, 0, s>>>(mat(&gate), mat(&up), rows8(q), gate.rows, gate.cols, g.cshift);
