@@ -11,7 +11,7 @@
 // power of two, so nothing overflows on the way.
 // Bound by memory, and close behind it by the arithmetic of a code (9 operations) and
 // of silu: 65536 x 2048 with its inputs kept forward 192 us, backward 182, one after the
-// other 345 (6.3 TB/s); 16384 x 7168 to codes 67 us and back 61, one after the other 117,
+// other 345 to 349 (6.3 TB/s); 16384 x 7168 to codes 67 us and back 61, one after the other 117,
 // by rows 66, 8192 x 7168 by rows 33; silu into codes 65536 x 2048 by rows 115 us, in
 // blocks 114.  (us a call, calls one after another on changing inputs.)  8 columns
 // a thread: 16 make a store past the cache half a line (the backward pass 299 us against
